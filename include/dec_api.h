@@ -325,6 +325,120 @@ dec_status ffn_gate_up(const void* Wgu, const float* x, const float* gain, float
 dec_status weight_gemv_q8(const void* Wq, const float* scale, const void* x, int32_t B, int32_t N, int32_t K,
                           float* y, dec_stream_t stream);
 
+/* ---------------------------------------------------------------- a step over a caller's paged cache
+ *
+ * The pieces of a serving step for programs that own the KV pool and the block table
+ * themselves (as gqa_decode_attn's callers do): paged_resize gives sequences their pages and
+ * every new row its slot, paged_rope_append stores the rows, gqa_chunk_attn attends any number
+ * of new rows a sequence, spec_verify keeps or rejects drafted tokens, and paged_resize takes
+ * the rejected rows' pages back. All lengths stay on the device, so a step of fixed buffer
+ * sizes can be captured into a CUDA graph and replayed with other lengths. Every call is
+ * stream-ordered and keeps nothing between calls; calls on different streams may overlap as
+ * long as their buffers, workspaces among them, are different. */
+
+/* Block tables and slot maps from sequence lengths. Sequence b goes from old_len[b] to
+ * new_len[b] cache rows; with held = ceil(old / 16) and want = ceil(new / 16) it takes
+ * want - held pages from the free list, or gives held - want back. Over all sequences, in the
+ * order (sequence, page): the i-th page taken is free_pages[F - 1 - i], then the k-th page
+ * given back goes to free_pages[F - A + R - 1 - k] (F = *n_free before, A pages taken, R given
+ * back; pages given back serve the next call). Resizing back therefore restores the table and
+ * the free list exactly.
+ *   old_len, new_len device int32 [B]
+ *   block_table device int32 [B][max_pages]: new pages' entries are set, those given back become -1
+ *   free_pages  device int32 [n_pages], the first *n_free of them free; n_free device int32 [1];
+ *               both updated
+ *   cu_rows     device int32 [B + 1], out: sequence b's new rows are cu_rows[b] .. cu_rows[b + 1] - 1
+ *               (none for a sequence that shrinks)
+ *   slot, row_pos device int32 [T], out: for each new row its cache slot 16 * page + offset and its
+ *               position; -1 from row cu_rows[B] on. A row whose table entry lies outside
+ *               [0, n_pages) gets slot -1.
+ *   status      device int32 [1], out: DEC_OK, or a failure after which table, free list and
+ *               n_free are unchanged, every slot and position is -1 and every row start 0:
+ *               DEC_ERR_INVALID_ARG (a negative length, *n_free outside [0, n_pages], more than T
+ *               new rows, more pages given back than the list holds, or a page that changes hands
+ *               outside [0, n_pages)), else DEC_ERR_CONTEXT_OVERFLOW (a length above
+ *               16 * max_pages), else DEC_ERR_PAGES_EXHAUSTED (A > F)
+ * Errors on the host: NULL pointer or a bad size -> INVALID_ARG; B > 4096, page_size other than
+ * 16 -> UNSUPPORTED. */
+dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t B, int32_t* block_table,
+                        int32_t max_pages, int32_t page_size, int32_t* free_pages, int32_t n_pages, int32_t* n_free,
+                        int32_t* cu_rows, int32_t* slot, int32_t* row_pos, int32_t T, int32_t* status,
+                        dec_stream_t stream);
+
+/* QK-norm, RoPE and cache append of T rows of the QKV projection (the prefill chunk's rotation
+ * and append, for any rows of any sequences).
+ *   qkv     device fp32 [T][ld], each row nq*d q values, nkv*d k values, nkv*d v values
+ *   q_norm, k_norm device fp32 [d] or NULL: per-head RMSNorm (eps) of q / of k before RoPE
+ *   slot    device int32 [T]: 16 * page + offset; a row whose slot lies outside [0, 16 * n_pages)
+ *           is skipped, its q_out row and the pool left as they were. Slots of rows that are not
+ *           skipped must differ.
+ *   row_pos device int32 [T]: position of the row (half-split pairs, angle
+ *           p * rope_base^(-2i/d), evaluated in fp64)
+ *   q_out   device bf16 [T][nq][d]; k_pool/v_pool device bf16 [n_pages][nkv][16][d]
+ * d must be 64 or 128, page_size 16. Errors: NULL pointer, a bad size or ld below
+ * (nq + 2 nkv) d -> INVALID_ARG; else UNSUPPORTED. T = 0 does nothing. */
+dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, const float* k_norm, float eps,
+                             float rope_base, const int32_t* slot, const int32_t* row_pos, int32_t T, int32_t nq,
+                             int32_t nkv, int32_t d, int32_t page_size, void* q_out, void* k_pool, void* v_pool,
+                             int32_t n_pages, dec_stream_t stream);
+
+/* Causal GQA attention of ragged chunks of new rows over the paged cache. Sequence b owns q
+ * rows cu_rows[b] .. cu_rows[b + 1] - 1 (n of them) and kv_len[b] cache rows, the new rows
+ * among them: row i of the n sits at position p = kv_len[b] - n + i and attends cache rows
+ * max(0, p - window + 1) .. p (0 .. p when window is 0),
+ *   out[r][h] = sum_j softmax_j(c(q[r][h] . K[j] * scale)) V[j],  kv head h / (nq/nkv),
+ * c(s) = softcap * tanh(s / softcap), or s when softcap is 0.
+ *   q       device bf16 [T] rows of [nq][d], row stride ldq elements (a multiple of 8)
+ *   k_pool/v_pool device bf16 [n_pages][nkv][16][d]; block_table device int32 [B][max_pages]
+ *   cu_rows device int32 [B + 1], ascending, within [0, T]; kv_len device int32 [B]
+ *   out     device bf16 [T][nq][d]; rows outside [cu_rows[0], cu_rows[B]) are left as they were
+ *   workspace device scratch of gqa_chunk_attn_workspace(d) bytes, 16-byte aligned; nothing in
+ *           it needs setting and nothing is kept in it
+ * A row that sees no key (a position below 0) gives zeros, and so does one whose scores are all
+ * -inf. A cache row whose table entry lies outside [0, n_pages) is not attended. Keys a row
+ * does not attend never reach it, whatever the pool holds there (NaN and infinities included).
+ * kv_len above 16 * max_pages counts as 16 * max_pages.
+ * Errors: NULL pointer, a bad size, scale not positive or ldq below nq*d -> INVALID_ARG; more
+ * than 16 query heads a kv head, d other than 64 / 128, page_size other than 16, B > 4096, or an
+ * address or stride off the 16-byte grid -> UNSUPPORTED. T = 0 does nothing. A device wait that
+ * runs out is reported by dec_check_standalone. */
+dec_status gqa_chunk_attn(const void* q, int64_t ldq, const void* k_pool, const void* v_pool, int32_t n_pages,
+                          const int32_t* block_table, int32_t max_pages, const int32_t* cu_rows,
+                          const int32_t* kv_len, int32_t B, int32_t T, int32_t nq, int32_t nkv, int32_t d,
+                          int32_t page_size, float scale, int32_t window, float softcap, void* out, void* workspace,
+                          int64_t workspace_bytes, dec_stream_t stream);
+int64_t gqa_chunk_attn_workspace(int32_t d);
+
+/* Verification of drafted tokens by the rejection rule of speculative sampling, from given
+ * uniform random numbers. Sequence b has n_b = n_draft[b] drafts x_0 .. ; p_i is the softmax of
+ * target row i / temperature[b] (row i: the logits that follow i accepted drafts, as dec_verify
+ * writes them), q_i the softmax of draft row i / temperature[b], or 1 at x_i when draft is NULL.
+ * Drafts are accepted while u_accept[b][i] * q_i(x_i) < p_i(x_i); a token outside [0, V) is
+ * not. The token after the accepted ones is the least j with w_j > 0 whose cumulative weight
+ * exceeds u_sample[b] * sum(w), with w = max(p_i - q_i, 0) at the rejected draft i (p_i when no
+ * weight is left) and w = p_{n_b} after the last draft. temperature[b] <= 0 is greedy: a draft
+ * is accepted when it is the argmax of its target row (lowest index on ties), the next token is
+ * the argmax. The accepted drafts' distribution followed by this token is the target's.
+ *   target  device fp32, row i of sequence b at target + b * target_seq + i * target_row, V values;
+ *           draft (or NULL) likewise, n rows a sequence. -inf is a token of no probability; +inf
+ *           and NaN are not allowed (no out-of-range access follows, but the tokens mean nothing)
+ *   draft_tok device int32 [B][n]; n_draft device int32 [B], taken into [0, n], or NULL: n
+ *   temperature device fp32 [B] or NULL: 1; u_accept device fp32 [B][n], u_sample device fp32 [B],
+ *           in [0, 1)
+ *   n_accepted device int32 [B], out; tokens device int32 [B][n + 1], out: the accepted drafts, the
+ *           next token (-1 when every logit is -inf), then -1
+ *   workspace device scratch of spec_verify_workspace(B, n, V) bytes, 16-byte aligned
+ * A sequence that held L cache rows and forwarded its last token and n_b drafts goes on with
+ * L + n_accepted + 1 rows (paged_resize or dec_truncate).
+ * Errors: NULL pointer, a bad size or stride -> INVALID_ARG; n > 64, B (2n + 1) > 65535 ->
+ * UNSUPPORTED. */
+dec_status spec_verify(const float* target, int64_t target_row, int64_t target_seq, const float* draft,
+                       int64_t draft_row, int64_t draft_seq, const int32_t* draft_tok, const int32_t* n_draft,
+                       const float* temperature, const float* u_accept, const float* u_sample, int32_t B, int32_t n,
+                       int32_t V, int32_t* n_accepted, int32_t* tokens, void* workspace, int64_t workspace_bytes,
+                       dec_stream_t stream);
+int64_t spec_verify_workspace(int32_t B, int32_t n, int32_t V);
+
 /* ---------------------------------------------------------------- test hooks */
 
 /* The n-th device allocation made by the library from now on fails as if the device
