@@ -106,6 +106,8 @@ def lib():
         L.dec_test_gemm_wait.argtypes = [_I, C.c_int64]
         L.dec_test_streamk_check.argtypes = [_I, _I, _I, _I]
         L.dec_test_streamk_check.restype = C.c_int
+        L.dec_test_chunk_split.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I]
+        L.dec_test_chunk_split.restype = C.c_int
         for f in ("dec_init", "dec_free", "dec_reset", "dec_prefill", "dec_step", "dec_last_argmax", "dec_kv_read",
                   "dec_kv_write", "dec_last_routes", "dec_last_hidden", "dec_seq_len", "gqa_decode_attn",
                   "gqa_decode_attn_noalloc", "moe_route_topk", "moe_experts", "weight_gemv", "dec_check",
@@ -532,6 +534,15 @@ def test_streamk_check(M: int, N: int, K: int, ctas: int) -> int:
     """Test hook: violations of the persistent GEMM's work-split invariants for an
     M x N x K product over `ctas` CTAs, checked on the host (0 = sound)."""
     return int(lib().dec_test_streamk_check(int(M), int(N), int(K), int(ctas)))
+
+
+def test_chunk_split(cu_rows, kv_len, max_pages: int, G: int, nkv: int, window: int = 0) -> int:
+    """Test hook: violations of gqa_chunk_attn's work split for these lengths, checked on the
+    host (0 = sound)."""
+    cu = np.ascontiguousarray(cu_rows, np.int32)
+    kv = np.ascontiguousarray(kv_len, np.int32)
+    return int(lib().dec_test_chunk_split(cu.ctypes.data, kv.ctypes.data, kv.size, int(max(cu[-1], 0)), max_pages, G,
+                                          nkv, window))
 
 
 def test_gemm_wait(extra_pieces: int, limit_cycles: int):

@@ -1539,6 +1539,9 @@ dec_status dec_check_standalone(dec_stream_t stream) {
     g_err.clear();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     CUDA_TRY(cudaStreamSynchronize(st));
+    int chunk = 0;
+    CUDA_TRY(chunk_take_error(&chunk));
+    if (chunk) return fail(DEC_ERR_TIMEOUT, "a bounded device wait of gqa_chunk_attn ran out; its output is not valid");
     std::lock_guard<std::mutex> lock(g_scratch_mu);
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1568,6 +1571,12 @@ dec_status dec_test_gemm_wait(int32_t extra_pieces, int64_t limit_cycles) {
 
 int32_t dec_test_streamk_check(int32_t M, int32_t N, int32_t K, int32_t ctas) {
     return gemm_streamk_check(M, N, K, ctas);
+}
+
+int32_t dec_test_chunk_split(const int32_t* cu_rows, const int32_t* kv_len, int32_t B, int32_t T, int32_t max_pages,
+                             int32_t G, int32_t nkv, int32_t window) {
+    if (!cu_rows || !kv_len || B <= 0 || T < 0 || max_pages <= 0 || G <= 0 || G > 16 || nkv <= 0 || window < 0) return -1;
+    return chunk_split_check(cu_rows, kv_len, B, T, max_pages, G, nkv, window);
 }
 
 }  // extern "C"

@@ -159,6 +159,11 @@ cudaError_t attn_prefill_launch(const AttnPrefillArgs& a, cudaStream_t st, bool 
 // The tensor-core prefill attention (tcgen05, TMEM): head dim 128, power-of-two groups.
 bool attn_prefill_tc_ok(const AttnPrefillArgs& a);
 cudaError_t attn_prefill_tc_launch(const AttnPrefillArgs& a, cudaStream_t st, bool pdl);
+// Whether a wait of gqa_chunk_attn's kernel ran out on the current device since the last call (clears it).
+cudaError_t chunk_take_error(int* set);
+// Host-side check of gqa_chunk_attn's work split (see attn_chunk.cu): violations.
+int chunk_split_check(const int32_t* cu, const int32_t* kv_len, int B, int T, int max_pages, int G, int nkv,
+                      int window);
 // A bf16 tensor map with 128-byte swizzle: dims[0] contiguous; strides[i] (bytes) of dims[i + 1].
 cudaError_t tmap_bf16_sw128(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
                             const uint64_t* strides, const uint32_t* box);

@@ -462,6 +462,12 @@ dec_status dec_test_gemm_wait(int32_t extra_pieces, int64_t limit_cycles);
  * non-positive argument. */
 int32_t dec_test_streamk_check(int32_t M, int32_t N, int32_t K, int32_t ctas);
 
+/* Host-side check (no GPU needed) of gqa_chunk_attn's work split for given lengths (host arrays
+ * here): every (tile, key block) is in one run once, and a tile cut between runs is joined from
+ * the run that starts it. Returns the number of violations (0 = sound), or -1 for a bad argument. */
+int32_t dec_test_chunk_split(const int32_t* cu_rows, const int32_t* kv_len, int32_t B, int32_t T, int32_t max_pages,
+                             int32_t G, int32_t nkv, int32_t window);
+
 /* Copy cache rows [pos0, pos0+n) of layer `layer` of sequence `seq` to / from host
  * buffers bf16 [n][nkv*d] (k and v). dec_kv_write also extends the sequence's length
  * to pos0+n when that is longer (allocating pages). Both synchronise. */

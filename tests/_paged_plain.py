@@ -95,6 +95,36 @@ def chunk_attn(q, kp, vp, table, cu, kv_len, scale, window=0, cap=0.0, out=None)
     return out, mag
 
 
+def chunk_attn_on_device(q, kp, vp, table, cu, kv_len, scale, window=0, cap=0.0):
+    """chunk_attn for long sequences: the same in 64-bit torch on q's device, one (sequence, kv
+    head, block of rows) at a time. Pools without NaN; every row in a sequence, every page good."""
+    import torch
+    T, nq, d = q.shape
+    nkv = kp.shape[1]
+    G = nq // nkv
+    out = torch.zeros((T, nq, d), dtype=torch.float64, device=q.device)
+    mag = torch.zeros_like(out)
+    for b in range(len(kv_len)):
+        L, n = int(kv_len[b]), int(cu[b + 1] - cu[b])
+        j = torch.arange(L, device=q.device)
+        pg = torch.as_tensor(table[b], device=q.device).long()[j // PAGE]
+        for g in range(nkv):
+            K, V = kp[pg, g, j % PAGE].double(), vp[pg, g, j % PAGE].double()
+            for r in range(0, n, 512):
+                i = torch.arange(r, min(n, r + 512), device=q.device)
+                p = (L - n + i)[:, None, None]
+                s = torch.einsum("tgd,jd->tgj", q[cu[b] + i, g * G:(g + 1) * G].double(), K) * scale
+                if cap > 0:
+                    s = cap * torch.tanh(s / cap)
+                hide = j > p
+                if window:
+                    hide = hide | (j <= p - window)
+                e = torch.softmax(s.masked_fill(hide, -float("inf")), -1)
+                out[cu[b] + i, g * G:(g + 1) * G] = e @ V
+                mag[cu[b] + i, g * G:(g + 1) * G] = e @ V.abs()
+    return out.cpu().numpy(), mag.cpu().numpy()
+
+
 def softmax(l):
     m = l.max()
     if m == -np.inf:

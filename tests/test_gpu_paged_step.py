@@ -186,7 +186,7 @@ def chunk_inputs(rows, nq, nkv, d, seed, extra_rows=0, holes=False):
     return q, kp, vp, table, cu, np.array([L for _, L in rows])
 
 
-def check_chunk(inp, scale=None, window=0, cap=0.0, q_view=None, workspace=None):
+def check_chunk(inp, scale=None, window=0, cap=0.0, q_view=None, workspace=None, on_device=False):
     q, kp, vp, table, cu, lens = inp
     T, nq, d = q.shape
     scale = float(np.float32(scale or 1 / math.sqrt(d)))
@@ -196,8 +196,12 @@ def check_chunk(inp, scale=None, window=0, cap=0.0, q_view=None, workspace=None)
                        window=window, softcap=cap, workspace=workspace)
     dec.check_standalone()
     nan0 = lambda t: np.nan_to_num(f64(t), nan=0.0)  # noqa: E731  (never attended: masked places)
-    want, mag = plain.chunk_attn(f64(q), nan0(kp), nan0(vp), table, cu, lens, scale, window,
-                                 float(np.float32(cap)), f64(start))
+    if on_device:
+        want, mag = plain.chunk_attn_on_device(q, torch.nan_to_num(kp), torch.nan_to_num(vp), table, cu, lens, scale,
+                                               window, float(np.float32(cap)))
+    else:
+        want, mag = plain.chunk_attn(f64(q), nan0(kp), nan0(vp), table, cu, lens, scale, window,
+                                     float(np.float32(cap)), f64(start))
     got = f64(out)
     assert np.isfinite(got).all()
     # half a bf16 step of the result; each weight rounded to bf16 (half a step, 2^-8 relative) and
@@ -246,6 +250,22 @@ def test_chunk_many_sequences():
 
 def test_chunk_mixed_prompts_and_decodes():
     check_chunk(chunk_inputs([(1, 700), (300, 300), (1, 5), (130, 900), (1, 2048), (8, 1500)], 8, 2, 128, 9))
+
+
+@pytest.mark.parametrize("rows,nq,nkv,d,window,cap", [
+    ([(1, 3000 + 37 * i) for i in range(30)], 32, 8, 128, 0, 0.0),             # many blocks and several tiles a run
+    ([(1 + i % 9, 2000 + 101 * i) for i in range(40)], 32, 8, 128, 0, 0.0),
+    ([(1, 128 * (1 + i)) for i in range(40)], 16, 16, 128, 0, 0.0),            # lengths at block borders
+    ([(2500, 4100)], 32, 8, 128, 0, 0.0),                                      # many tiles a run
+    ([(3000, 3000), (1, 9000), (700, 2000)], 16, 16, 128, 0, 0.0),
+    ([(1500, 2500), (1, 3000), (1100, 1100)], 16, 16, 128, 1024, 50.0),
+    ([(2000, 2600), (5, 5000)] + [(1, 777)] * 30, 9, 3, 64, 0, 0.0),
+    ([(2000, 2600), (5, 5000)] + [(1, 777)] * 30, 9, 3, 64, 130, 0.0),
+    ([(900, 5000)], 24, 2, 128, 0, 100.0),
+    ([(1, 20000), (16, 9000)], 16, 1, 128, 0, 0.0)],
+    ids=lambda v: f"{len(v)}seqs" if isinstance(v, list) else str(v))
+def test_chunk_long(rows, nq, nkv, d, window, cap):
+    check_chunk(chunk_inputs(rows, nq, nkv, d, len(rows) + nq), window=window, cap=cap, on_device=True)
 
 
 def test_chunk_strided_q_rows():
