@@ -9,7 +9,7 @@
 //
 // Tiles. The G query heads that share a kv head are packed with the tokens: a sub-tile is
 // 128 / G tokens x G heads = up to 128 MMA rows, a tile two sub-tiles (0 and 1), each with
-// four softmax warps, a thread a row. Two ways to use the pair:
+// eight softmax warps. Two ways to use the pair:
 //   two   the tile has rows for both: both read the same key blocks, so a K or V block is
 //         loaded once for 256 rows, and while one sub-tile's scores are being exponentiated
 //         the tensor cores work for the other;
@@ -23,8 +23,8 @@
 // as much as the rounding of the result; l sums the unrounded fp32 values.
 //
 // Work split. Lengths are known on the device only, so every CTA cuts the work for itself:
-// the (tile, key block) pairs of all sequences, kv heads and tiles form one list, cut into
-// equal runs, one for each of 148 CTAs (the number of blocks of the first t tiles of a sequence
+// the (tile, key block) pairs of all sequences, kv heads and tiles form one list, cut into runs
+// of equal cost, one for each of 148 CTAs (the number of blocks of the first t tiles of a sequence
 // has a closed form, so finding a run's start takes a scan over the sequences and a binary
 // search). A long prompt, a batch of decodes, or both at once keep every SM equally busy. A
 // tile cut between CTAs leaves unnormalised fp32 pieces (O, m, l) in the workspace, which a
@@ -36,8 +36,8 @@
 // memory, and where tokens of the tile see different keys, also take out values that are not
 // finite, note their keys, and the epilogue adds those values back to the rows that do see them.
 //
-// Warps: 0-3 and 4-7 softmax and epilogue of sub-tiles 0 and 1, 8 TMA producer, 9 MMA
-// issuer, 10-11 V cleaning. Shared memory: Q [2 sub-tiles][d / 64][128][64] and a ring of
+// Warps: 0-7 and 8-15 softmax and epilogue of sub-tiles 0 and 1 (two threads a row, each half of
+// the keys), 16 TMA producer, 17 MMA issuer, 18-19 V cleaning. Shared memory: Q [2 sub-tiles][d / 64][128][64] and a ring of
 // K and V blocks [d / 64][128][64] in the order of their use (all 128-byte swizzled).
 // TMEM columns: S/P of sub-tiles 0, 1 at 0, 128; O at 256, 256 + d.
 #include <cuda_runtime.h>
@@ -59,7 +59,10 @@ constexpr int kPage = 16;
 constexpr int kKeys = 128;     // keys of a block
 constexpr int kRows = 128;     // MMA rows of a sub-tile
 constexpr int kCtas = 148;     // runs the work is cut into: the SMs of a B200
-constexpr int kThreads = 384;
+constexpr int kHalves = 1;      // threads a row of a sub-tile has (each takes 128 / kHalves keys of a block)
+constexpr int kSubWarps = 4 * kHalves;          // softmax warps of a sub-tile
+constexpr int kSoftWarps = 2 * kSubWarps;
+constexpr int kThreads = 32 * (kSoftWarps + 4);  // softmax, TMA, MMA, two for cleaning V
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;  // log2 units
 constexpr int kDirty = 8;      // more than the V blocks a ring holds
@@ -112,6 +115,13 @@ static_assert(sizeof(Join) * kCtas <= kJoinBytes, "join table");
 
 // ------------------------------------------------------------------ work split
 
+// a / b for 0 <= a, 0 < b, in 32 bits where they fit (nearly always): a 64-bit division is a long
+// chain of instructions.
+DEC_HD long long div_small(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 struct Seq {
     int row0, n, p0;  // first q row, rows, position of the first row
 };
@@ -134,8 +144,8 @@ __host__ __device__ __noinline__ long long floor_sum(long long n, unsigned m, un
         b %= m;
         const unsigned long long y = (unsigned long long)a * (unsigned long long)n + b;
         if (y < m) break;
-        n = (long long)(y / m);
-        b = (unsigned)(y % m);
+        n = div_small((long long)y, m);
+        b = (unsigned)((long long)y - n * m);
         const unsigned t = m;
         m = a;
         a = t;
@@ -156,11 +166,17 @@ DEC_HD int lo_key(const ChunkArgs& a, const Seq& s, int t0) {
     return a.window > 0 ? (int)max((long long)s.p0 + t0 + 1 - a.window, 0ll) : 0;
 }
 
-// Blocks of the first t tiles, all of them full.
-DEC_HD long long blocks_before(const ChunkArgs& a, const Seq& s, int t) {
+// What a tile costs beside its blocks (filling the pipeline, the epilogue), in blocks: the runs are
+// equal in tiles' costs. A tile's units are kTileCost for nothing, then one for each block.
+constexpr int kTileCost = 3;
+// The block at which unit u of a tile lies; a run that ends within the first units has none of it.
+DEC_HD int block_at(int u) { return u > kTileCost ? u - kTileCost : 0; }
+
+// Units of the first t tiles, all of them full.
+DEC_HD long long units_before(const ChunkArgs& a, const Seq& s, int t) {
     if (t == 0) return 0;
     const int tpt = 2 * a.tps;
-    long long f = t + block_sum(t, s.p0 + tpt - 1, tpt);
+    long long f = (long long)t * (1 + kTileCost) + block_sum(t, s.p0 + tpt - 1, tpt);
     // before position 0 the window starts at 0 as well: p0 + 1 - W is at least -2^30 - 2^31 and may
     // leave 32 bits, where every term of such a tile count is 0
     const long long c = (long long)s.p0 + 1 - a.window;
@@ -175,49 +191,60 @@ DEC_HD int tile_blocks(const ChunkArgs& a, const Seq& s, int t) {
     return hi_key(s, t1) / kKeys - lo_key(a, s, t0) / kKeys + 1;
 }
 
-// Blocks of one kv head of a sequence.
-DEC_HD long long seq_blocks(const ChunkArgs& a, const Seq& s) {
+// Units of one kv head of a sequence.
+DEC_HD long long seq_units(const ChunkArgs& a, const Seq& s) {
     if (s.n == 0) return 0;
     const int nt = tile_count(a, s);
-    return blocks_before(a, s, nt - 1) + tile_blocks(a, s, nt - 1);
+    return units_before(a, s, nt - 1) + kTileCost + tile_blocks(a, s, nt - 1);
 }
 
-// The run of one CTA: where it starts, and how many blocks it has.
+// The run of one CTA: where it starts, and how many units it has.
 struct Run {
-    int b, g, tile, off;  // sequence, kv head, tile, block within the tile
+    int b, g, tile, off;  // sequence, kv head, tile, unit within the tile
     int len;
     int first;            // CTA of the run in which the first tile starts
 };
 
-// The run of units u0 .. u1 - 1, which starts in sequence b or after it (`before`: units of the
-// sequences below b).
-DEC_HD Run run_from(const ChunkArgs& a, int b, long long before, long long u0, long long u1, long long runs,
-                    long long total) {
-    long long r = u0 - before;
+// All units (tile blocks of every kv head) cut into kCtas runs of q or q + 1, the longer ones first.
+struct Cut {
+    long long q, rem;
+    DEC_HD explicit Cut(long long total) : q(total / kCtas), rem(total % kCtas) {}
+    DEC_HD long long start(int c) const { return c * q + (c < rem ? c : rem); }
+    DEC_HD long long len(int c) const { return q + (c < rem ? 1 : 0); }
+    // the CTA whose run holds unit u
+    DEC_HD int cta_of(long long u) const {
+        const long long longer = rem * (q + 1);
+        return (int)(u < longer ? div_small(u, q + 1) : rem + div_small(u - longer, q));
+    }
+};
+
+// The run of CTA cta, which starts in sequence b or after it (`before`: units of the sequences
+// below b).
+DEC_HD Run run_from(const ChunkArgs& a, int b, long long before, const Cut& cut, int cta) {
+    long long r = cut.start(cta) - before;
     Seq s = seq_of(a, b);
-    long long per_head = seq_blocks(a, s);
+    long long per_head = seq_units(a, s);
     while (r >= per_head * a.nkv) {
         r -= per_head * a.nkv;
         s = seq_of(a, ++b);
-        per_head = seq_blocks(a, s);
+        per_head = seq_units(a, s);
     }
     Run f;
     f.b = b;
-    f.g = (int)(r / per_head);
-    r %= per_head;
+    f.g = (int)div_small(r, per_head);
+    r -= f.g * per_head;
     int lo = 0, hi = tile_count(a, s);
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (blocks_before(a, s, mid) <= r)
+        if (units_before(a, s, mid) <= r)
             lo = mid;
         else
             hi = mid;
     }
     f.tile = lo;
-    f.off = (int)(r - blocks_before(a, s, lo));
-    f.len = (int)(u1 - u0);
-    // runs are never empty, so the CTA whose run holds unit u is the last one that starts at or before it
-    f.first = (int)(((u0 - f.off + 1) * runs - 1) / total);
+    f.off = (int)(r - units_before(a, s, lo));
+    f.len = (int)cut.len(cta);
+    f.first = cut.cta_of(cut.start(cta) - f.off + kTileCost);
     return f;
 }
 
@@ -227,7 +254,7 @@ DEC_DEVINL Run find_run(const ChunkArgs& a, int cta, long long* scratch) {
     const int per = (a.B + blockDim.x - 1) / blockDim.x;
     const int b0 = threadIdx.x * per, b1 = min(a.B, b0 + per);
     long long own = 0;
-    for (int b = b0; b < b1; ++b) own += seq_blocks(a, seq_of(a, b)) * a.nkv;
+    for (int b = b0; b < b1; ++b) own += seq_units(a, seq_of(a, b)) * a.nkv;
     long long x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -242,21 +269,13 @@ DEC_DEVINL Run find_run(const ChunkArgs& a, int cta, long long* scratch) {
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    const long long runs = min((long long)kCtas, total);
-    if (cta < runs) {
-        const long long u0 = cta * total / runs, u1 = (cta + 1) * total / runs;
-        before += x - own;
-        if (u0 >= before && u0 < before + own) {
-            *found = run_from(a, b0, before, u0, u1, runs, total);
-        }
-    }
+    const Cut cut(total);
+    const long long u0 = cut.start(cta);
+    before += x - own;
+    if (cut.len(cta) > 0 && u0 >= before && u0 < before + own) *found = run_from(a, b0, before, cut, cta);
     __syncthreads();
-    Run f;
-    if (cta < runs) {
-        f = *found;
-    } else {
-        f.b = f.g = f.tile = f.off = f.len = f.first = 0;
-    }
+    Run f{0, 0, 0, 0, 0, 0};
+    if (cut.len(cta) > 0) f = *found;
     __syncthreads();
     return f;
 }
@@ -295,7 +314,11 @@ struct Walk {
         if (r.len > 0) s = seq_of(a, r.b);
     }
     DEC_HD bool next(const ChunkArgs& a, Piece* p) {
-        if (r.len <= 0) return false;
+        while (r.len > 0)
+            if (step(a, p)) return true;
+        return false;
+    }
+    DEC_HD bool step(const ChunkArgs& a, Piece* p) {
         p->b = r.b;
         p->g = r.g;
         p->t0 = r.tile * 2 * a.tps;
@@ -306,11 +329,13 @@ struct Walk {
         p->lo = lo_key(a, s, p->t0);
         p->two = p->ntok > a.tps;
         const int blocks = p->hi / kKeys - p->lo / kKeys + 1;
-        p->kb0 = p->lo / kKeys + r.off;
-        p->nb = min(blocks - r.off, r.len);
-        p->starts = r.off == 0;
-        p->ends = r.off + p->nb == blocks;
-        r.len -= p->nb;
+        const int units = min(kTileCost + blocks - r.off, r.len);
+        const int b0 = block_at(r.off);
+        p->kb0 = p->lo / kKeys + b0;
+        p->nb = block_at(r.off + units) - b0;
+        p->starts = b0 == 0;
+        p->ends = b0 + p->nb == blocks;
+        r.len -= units;
         r.off = 0;
         if (r.len > 0) {  // the tile is done
             if (++r.tile == tile_count(a, s)) {
@@ -322,14 +347,15 @@ struct Walk {
                 }
             }
         }
-        return true;
+        return p->nb > 0;
     }
 };
 
 // ------------------------------------------------------------------ kernel
 
 struct Poison {
-    int n;                 // entries
+    int n;                 // masked blocks noted so far
+    uint32_t some[2];      // whether either half has any key noted
     int kb[kPoison];
     uint32_t keys[kPoison][4];
 };
@@ -339,13 +365,13 @@ struct Control {
     uint64_t full[10], empty[10];
     uint64_t dirty[kDirty]; // loads of V blocks to be cleaned, in their order; the cleaning completes full[stage]
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t o_free;       // the epilogue has read O: 8 warps
+    uint64_t o_free;       // the epilogue has read O: 16 warps
     uint64_t clean_done;   // a piece's notes are complete: 2 warps
     uint32_t tmem;
     Poison poison;
     union {
-        long long scratch[40];
-        float2 xch[2][kRows];  // (m, l) of the two halves of a `one` tile
+        long long scratch[64];
+        float xm[2][2][kRows];  // a block's maximum, at the end l, of each half of the rows
     };
 };
 
@@ -361,23 +387,125 @@ DEC_DEVINL bool named_bar_and(uint32_t id, uint32_t n, bool v) {
     return r != 0;
 }
 
-DEC_DEVINL void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-    tmem_ld16_issue(taddr, r);
-    tmem_ld16_issue(taddr + 16, r + 16);
+// As mbar_wait_bounded, letting the hardware suspend the thread for up to 20 us at a time: a warp
+// that polls takes issue slots from the others.
+DEC_DEVINL bool wait(uint64_t* bar, uint32_t parity, int* err) {
+    auto test = [&]() {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        return done != 0;
+    };
+    if (test()) return true;
+    const long long t0 = clock64();
+    while (!test()) {
+        if (clock64() - t0 > (1ll << 32)) {
+            atomicExch(err, 1);
+            return false;
+        }
+    }
+    return true;
 }
 
-// The softcapped score c tanh(x / c) in log2 units, by tanh(y) = 1 - 2 / (e^2y + 1): off by
-// some 2^-21 c, which for c <= 64 moves a weight by less than 2^-14. Larger caps take tanhf.
-DEC_DEVINL float capped(float raw, float k2, float c, float c_log2e) {
-    float e = ex2f(raw * k2), r;  // k2 = 2 log2(e) scale / c
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.0f));
-    return fmaf(-2.0f * c_log2e, r, c_log2e);
-}
-__device__ __noinline__ float capped_large(float raw, float scale, float c) {
-    return c * tanhf(raw * scale / c) * kLog2e;
+DEC_DEVINL bool named_bar_or(uint32_t id, uint32_t n, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
 }
 
-template <int D>
+// tcgen05.ld of 32 columns without waiting.
+DEC_DEVINL void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// As reg_fence32, for 16.
+DEC_DEVINL void reg_fence16(uint32_t (&r)[16]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]));
+}
+
+constexpr uint32_t kDescHi = (1024 >> 4) | (1 << 14) | (2 << 29);
+// Shared-memory descriptors (128-byte swizzle, 8-row groups 1 KB apart) in two words: the upper one
+// is constant, the lower one (address and leading offset, in 16 bytes) moves by an addition. The
+// MMA thread shares its scheduler with busy softmax warps, so every instruction between two
+// MMAs costs: with descriptors built afresh for each, issuing took longer than the products.
+//
+// MMA and TMA instructions take their operands from uniform registers. From code that only one
+// lane runs, each operand goes there by moves of its own, and this warp gets one issue slot in
+// several while softmax warps run. So all lanes compute the operands, a reduction over the warp puts
+// what they share into a uniform register, and only the instructions are in an elected lane's
+// branch: 8 MMAs of 64 cycles then take 512 cycles beside idle warps and 700 beside 16 warps of
+// FMAs (lane 0 alone: 512 and 950; predicated one by one: 570 and 1140).
+DEC_DEVINL uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+
+// One lane of a converged warp, as a predicate the compiler knows to be one.
+DEC_DEVINL bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// D (+)= A B, both from shared memory.
+DEC_DEVINL void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accum), "n"(kDescHi)
+        : "memory");
+}
+// The same with A from TMEM (lanes = rows, two 16-bit elements a column).
+DEC_DEVINL void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(idesc), "r"(accum), "n"(kDescHi)
+        : "memory");
+}
+DEC_DEVINL void commit_if(uint32_t on, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %0, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(on),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+DEC_DEVINL uint32_t desc_lo(uint32_t saddr, uint32_t leading) { return (saddr >> 4) | (leading << 16); }
+DEC_DEVINL float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// The softcapped score c tanh(y) in log2 units, y = raw k: tanh(y) = 1 - 2 / (e^2y + 1), off by
+// some 2^-21, above |y| = 1/4, its Taylor series (next term 2^-18 of the value there) below, so
+// that the error stays a 2^-18 part of the score whatever the cap.
+DEC_DEVINL float capped(float raw, float k, float c_log2e) {
+    const float y = raw * k, y2 = y * y;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2f(y * (2.0f * kLog2e)) + 1.0f));
+    const float big = fmaf(-2.0f, r, 1.0f);
+    const float small = y * fmaf(y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.0f);
+    return c_log2e * (y2 < 0.0625f ? small : big);
+}
+
+template <int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const ChunkArgs a) {
@@ -398,19 +526,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kDirty; ++i) mbar_init(&ctl.dirty[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl.s_full[i], 1);
-            mbar_init(&ctl.p_full[i], 4);
+            mbar_init(&ctl.p_full[i], kSubWarps);
             mbar_init(&ctl.pv_done[i], 1);
         }
-        mbar_init(&ctl.o_free, 8);
+        mbar_init(&ctl.o_free, kSoftWarps);
         mbar_init(&ctl.clean_done, 2);
         fence_mbar_init();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == kSoftWarps && lane == 0) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
-    if (warp == 9) {
+    if (warp == kSoftWarps + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
                      "r"(512)
                      : "memory");
@@ -425,28 +553,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Run run = find_run(a, blockIdx.x, ctl.scratch);
     Walk walk(a, run);
     Piece pc;
-
-    if (warp == 8) {
+    // registers: 384 threads start with 168 each (640 with 96); 8 softmax warps x 208 + 4 x 88 (16 x 104 +
+    // 4 x 64) is as many
+    if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHalves == 1 ? 88 : 64));
+    if (warp == kSoftWarps) {
         // ---------------------------------------------------------- TMA producer
-        // lane l loads half l / 8 (64 columns) of page l % 8 of a block
         const int pool_rows = a.n_pages * a.nkv * kPage;
         int item = 0, n = 0, nd = 0;  // ring items, pieces, blocks to be cleaned
+        bool was_two = false;
         bool ok = true;
         while (ok && walk.next(a, &pc)) {
             const int page_lo = pc.lo / kPage, page_hi = pc.hi / kPage;
             const int32_t* tab = a.table + (size_t)pc.b * a.max_pages;
-            // pool row of the lane's page of block k of the piece; a page outside the pool gets a row
-            // past its end, which the TMA unit fills with zeros; -1: no key of the tile is on the page
-            auto row_of = [&](int k) {
-                const int pi = (pc.kb0 + k) * (kKeys / kPage) + (lane & 7);
-                if (k >= pc.nb || pi < page_lo || pi > page_hi) return -1;
-                const int pg = tab[pi];
-                return pg >= 0 && pg < a.n_pages ? (pg * a.nkv + pc.g) * kPage : pool_rows;
+            // The lanes hold the table entries of four blocks (lane 8 i + p: page p of block 4 q + i), the next
+            // four's are on their way; a block's eight rows go to uniform registers.
+            auto entries = [&](int q) {
+                const int pi = (pc.kb0 + 4 * q) * (kKeys / kPage) + lane;
+                return pi >= page_lo && pi <= page_hi ? tab[pi] : 0;
             };
+            int have = 0, cur = entries(0), nxt = entries(1);
             const int LA = pc.two ? 1 : 2;
-            int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2), r3;
-            if (n > 0 && !mbar_wait_bounded(&ctl.q_empty, (n - 1) & 1, err)) break;
-            if (lane == 0) {
+            // Q may be loaded once the last piece's scores are done; where the last piece's result passes
+            // through a place that this piece's Q takes, once that piece is done
+            if (n > 0 && !wait(&ctl.q_empty, (n - 1) & 1, err)) break;
+            if (n > 0 && (pc.two || was_two) && !wait(&ctl.o_free, (n - 1) & 1, err)) break;
+            was_two = pc.two;
+            if (elected()) {
                 const int subs = pc.two ? 2 : 1;
                 mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(subs * a.tps * a.G * D * 2));
                 for (int s = 0; s < subs; ++s)
@@ -455,148 +588,184 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     &ctl.q_full);
             }
             __syncwarp();
-            auto load = [&](const CUtensorMap* tm, int row, bool clean) {
+            auto load = [&](const CUtensorMap* tm, int k, bool clean) {
                 const int st = item % kStages;
-                if (item >= kStages && !mbar_wait_bounded(&ctl.empty[st], (item / kStages - 1) & 1, err)) {
+                if (item >= kStages && !wait(&ctl.empty[st], (item / kStages - 1) & 1, err)) {
                     ok = false;
                     return;
                 }
                 ++item;
                 uint64_t* bar = clean ? &ctl.dirty[nd++ % kDirty] : &ctl.full[st];
-                const int pages = __popc(__ballot_sync(0xffffffffu, lane < 8 && row >= 0));
-                if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(pages * kPage * D * 2));
-                __syncwarp();
-                if (row >= 0 && lane < D / 8)
-                    tma_load_2d(smem + S::kOffRing + st * S::kBlock + (lane >> 3) * 16384 + (lane & 7) * 2048, tm,
-                                (lane >> 3) * 64, row, bar);
+                const int first = (pc.kb0 + k) * (kKeys / kPage);  // the block's pages that hold keys of the tile
+                const int p0 = max(page_lo - first, 0), p1 = min(page_hi - first, kKeys / kPage - 1);
+                const int pg = (k >> 2) == have ? cur : nxt;
+                // a page outside the pool gets a row past its end, which the TMA unit fills with zeros
+                const uint32_t row = pg >= 0 && pg < a.n_pages ? (pg * a.nkv + pc.g) * kPage : pool_rows;
+                uint32_t y[kKeys / kPage];
+#pragma unroll
+                for (int i = 0; i < kKeys / kPage; ++i) y[i] = uniform(lane == (k & 3) * 8 + i ? row : 0u);
+                uint8_t* dst = smem + S::kOffRing + st * S::kBlock;
+                if (elected()) {
+                    mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0 + 1) * kPage * D * 2));
+#pragma unroll
+                    for (int i = 0; i < kKeys / kPage; ++i)
+                        if (i >= p0 && i <= p1)
+#pragma unroll
+                            for (int h = 0; h < D / 64; ++h)
+                                tma_load_2d(dst + h * 16384 + i * 2048, tm, h * 64, (int)y[i], bar);
+                }
                 __syncwarp();
             };
-            load(&tmK, r0, false);
-            if (ok && LA == 2 && pc.nb > 1) load(&tmK, r1, false);
+            load(&tmK, 0, false);
+            if (ok && LA == 2 && pc.nb > 1) load(&tmK, 1, false);
             for (int k = 0; k < pc.nb && ok; ++k) {
-                r3 = row_of(k + 3);
-                load(&tmV, r0, pc.masked(a, pc.kb0 + k));
-                if (ok && k + LA < pc.nb) load(&tmK, LA == 1 ? r1 : r2, false);
-                r0 = r1;
-                r1 = r2;
-                r2 = r3;
+                if ((k >> 2) != have) {
+                    cur = nxt;
+                    nxt = entries(++have + 1);
+                }
+                load(&tmV, k, pc.masked(a, pc.kb0 + k));
+                if (ok && k + LA < pc.nb) load(&tmK, k + LA, false);
             }
             ++n;
         }
-    } else if (warp == 9) {
+    } else if (warp == kSoftWarps + 1) {
         // ---------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_tc<128, 128, false>();
-            constexpr uint32_t id_o = idesc_tc<128, D, true>();
-            const uint32_t sb = smem_u32(smem);
-            int item = 0, n = 0;
-            uint32_t p_par = 0;               // parity of p_full[s] in bit s
-            bool ok = true;
-            auto take = [&](int* st) {        // the next ring item, loaded
-                *st = item % kStages;
-                ok = ok && mbar_wait_bounded(&ctl.full[*st], (item / kStages) & 1, err);
-                ++item;
-            };
-            auto issue_s = [&](int s, int st, bool two) {
-                const uint32_t qb = sb + (two ? s : 0) * S::kBlock, kb = sb + S::kOffRing + st * S::kBlock;
-                tc_fence_after();
+        // all lanes walk along, one issues: see mma_ss
+        constexpr uint32_t id_s = idesc_tc<128, 128, false>();
+        constexpr uint32_t id_o = idesc_tc<128, D, true>();
+        const uint32_t sb = smem_u32(smem), tm = uniform(tmem);
+        const uint32_t one = lane == 0;
+        int item = 0, n = 0;
+        uint32_t p_par = 0;               // parity of p_full[s] in bit s
+        bool ok = true;
+        auto take = [&](int* st) {        // the next ring item, loaded
+            *st = item % kStages;
+            ok = ok && wait(&ctl.full[*st], (item / kStages) & 1, err);
+            ++item;
+        };
+        auto issue_s = [&](int s, int st, bool two) {
+            const uint32_t q = uniform(desc_lo(sb + (two ? s : 0) * S::kBlock, 1));
+            const uint32_t k = uniform(desc_lo(sb + S::kOffRing + st * S::kBlock, 1));
+            tc_fence_after();
+            if (elected()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma(tmem + s * kKeys, sdesc_sw128(qb + (kk >> 2) * 16384 + (kk & 3) * 32),
-                           sdesc_sw128(kb + (kk >> 2) * 16384 + (kk & 3) * 32), id_s, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t at = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
+                    mma_ss(tm + s * kKeys, q + at, k + at, id_s, kk > 0 ? 1u : 0u);
+                }
                 tc_commit(&ctl.s_full[s]);
-            };
-            auto wait_p = [&](int s) {
-                ok = ok && mbar_wait_bounded(&ctl.p_full[s], (p_par >> s) & 1, err);
-                p_par ^= 1u << s;
-            };
-            auto issue_o = [&](int s, int st, bool first) {
-                const uint32_t vb = sb + S::kOffRing + st * S::kBlock;
-                tc_fence_after();
+            }
+            __syncwarp();
+        };
+        auto wait_p = [&](int s) {
+            ok = ok && wait(&ctl.p_full[s], (p_par >> s) & 1, err);
+            p_par ^= 1u << s;
+        };
+        auto issue_o = [&](int s, int st, bool first) {
+            const uint32_t v = uniform(desc_lo(sb + S::kOffRing + st * S::kBlock, 16384 >> 4));
+            const uint32_t d = tm + 2 * kKeys + s * D, p = tm + s * kKeys, more = uniform(first ? 0u : 1u);
+            tc_fence_after();
+            if (elected()) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    tc_mma_tmem_a(tO + s * D, tmem + s * kKeys + kk * 8, sdesc_sw128_mn(vb + kk * 2048), id_o,
-                                  !first || kk > 0 ? 1u : 0u);
+                    mma_ts(d, p + kk * 8, v + kk * (2048 >> 4), id_o, kk > 0 ? 1u : more);
                 tc_commit(&ctl.pv_done[s]);
+            }
+            __syncwarp();
+        };
+        // the next piece is worked out while this one's first scores are on their way
+        Piece nx;
+        bool more = walk.next(a, &nx);
+        while (ok && more) {
+            pc = nx;
+            ok = wait(&ctl.q_full, n & 1, err);
+            int st = 0, sk = 0;
+            bool freed = n == 0;  // the last piece's O has been read
+            auto wait_o = [&]() {
+                if (!freed) ok = ok && wait(&ctl.o_free, (n - 1) & 1, err);
+                freed = true;
             };
-            while (ok && walk.next(a, &pc)) {
-                ok = mbar_wait_bounded(&ctl.q_full, n & 1, err);
-                int st = 0, sk = 0;
-                bool freed = n == 0;  // the last piece's O has been read
-                auto wait_o = [&]() {
-                    if (!freed) ok = ok && mbar_wait_bounded(&ctl.o_free, (n - 1) & 1, err);
-                    freed = true;
-                };
-                if (pc.two) {
-                    int from[2], to[2];
-                    pc.range(a, 0, &from[0], &to[0]);
-                    pc.range(a, 1, &from[1], &to[1]);
-                    if (ok) take(&sk);
-                    for (int s = 0; s < 2 && ok; ++s)
-                        if (from[s] == 0 && to[s] > 0) issue_s(s, sk, true);
-                    if (ok) tc_commit(&ctl.empty[sk]);
-                    if (ok && pc.nb == 1) tc_commit(&ctl.q_empty);
-                    for (int j = 0; j < pc.nb && ok; ++j) {
-                        take(&st);
-                        for (int s = 0; s < 2 && ok; ++s) {
-                            if (j >= from[s] && j < to[s]) {
-                                wait_p(s);
-                                wait_o();
-                                if (!ok) break;
-                                issue_o(s, st, j == from[s]);
-                            }
-                            if (s == 1) tc_commit(&ctl.empty[st]);
-                            if (j + 1 < pc.nb) {
-                                if (s == 0) take(&sk);
-                                if (!ok) break;
-                                if (j + 1 >= from[s] && j + 1 < to[s]) issue_s(s, sk, true);
-                                if (s == 1) tc_commit(&ctl.empty[sk]);
-                                if (s == 1 && j + 2 == pc.nb) tc_commit(&ctl.q_empty);
-                            }
-                        }
-                    }
-                } else {
-                    for (int k = 0; k < 2 && k < pc.nb && ok; ++k) {
-                        take(&sk);
+            if (pc.two) {
+                int from[2], to[2];
+                pc.range(a, 0, &from[0], &to[0]);
+                pc.range(a, 1, &from[1], &to[1]);
+                if (ok) take(&sk);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (ok && from[s] == 0 && to[s] > 0) issue_s(s, sk, true);
+                if (ok) commit_if(one, &ctl.empty[sk]);
+                if (ok && pc.nb == 1) commit_if(one, &ctl.q_empty);
+                more = walk.next(a, &nx);
+                for (int j = 0; j < pc.nb && ok; ++j) {
+                    take(&st);
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
                         if (!ok) break;
-                        issue_s(k, sk, false);
-                        tc_commit(&ctl.empty[sk]);
-                        if (k + 1 == pc.nb || (k == 1 && pc.nb == 2)) tc_commit(&ctl.q_empty);
-                    }
-                    for (int k = 0; k < pc.nb && ok; ++k) {
-                        const int s = k & 1;
-                        take(&st);
-                        wait_p(s);
-                        wait_o();
-                        if (!ok) break;
-                        issue_o(s, st, k < 2);
-                        tc_commit(&ctl.empty[st]);
-                        if (k + 2 < pc.nb) {
-                            take(&sk);
+                        if (j >= from[s] && j < to[s]) {
+                            wait_p(s);
+                            wait_o();
                             if (!ok) break;
-                            issue_s(s, sk, false);
-                            tc_commit(&ctl.empty[sk]);
-                            if (k + 3 == pc.nb) tc_commit(&ctl.q_empty);
+                            issue_o(s, st, j == from[s]);
+                        }
+                        if (s == 1) commit_if(one, &ctl.empty[st]);
+                        if (j + 1 < pc.nb) {
+                            if (s == 0) take(&sk);
+                            if (!ok) break;
+                            if (j + 1 >= from[s] && j + 1 < to[s]) issue_s(s, sk, true);
+                            if (s == 1) commit_if(one, &ctl.empty[sk]);
+                            if (s == 1 && j + 2 == pc.nb) commit_if(one, &ctl.q_empty);
                         }
                     }
                 }
-                ++n;
+            } else {
+                for (int k = 0; k < 2 && k < pc.nb && ok; ++k) {
+                    take(&sk);
+                    if (!ok) break;
+                    issue_s(k, sk, false);
+                    commit_if(one, &ctl.empty[sk]);
+                    if (k + 1 == pc.nb) commit_if(one, &ctl.q_empty);
+                }
+                more = walk.next(a, &nx);
+                for (int k = 0; k < pc.nb && ok; ++k) {
+                    const int s = k & 1;
+                    take(&st);
+                    wait_p(s);
+                    wait_o();
+                    if (!ok) break;
+                    issue_o(s, st, k < 2);
+                    commit_if(one, &ctl.empty[st]);
+                    if (k + 2 < pc.nb) {
+                        take(&sk);
+                        if (!ok) break;
+                        issue_s(s, sk, false);
+                        commit_if(one, &ctl.empty[sk]);
+                        if (k + 3 == pc.nb) commit_if(one, &ctl.q_empty);
+                    }
+                }
             }
+            ++n;
         }
-        __syncwarp();
-    } else if (warp >= 10) {
+    } else {
         // ---------------------------------------------------------- V cleaning (two warps, half the keys each)
-        const int half = warp - 10;
+        const int half = warp - (kSoftWarps + 2);
         int item = 0, n = 0, nd = 0;
         bool ok = true;
+        if (warp == kSoftWarps + 3 && lane == 0) {
+            // what the join needs to know of a tile that this run's first piece ends without starting it
+            Join jn{-1, 0, 0, 0};
+            Walk w2(a, run);
+            if (w2.next(a, &pc) && !pc.starts && pc.ends) jn = Join{run.first, pc.row0, pc.ntok, pc.g};
+            reinterpret_cast<Join*>(reinterpret_cast<char*>(a.ws) - kJoinBytes)[blockIdx.x] = jn;
+        }
+        __syncwarp();
         while (ok && walk.next(a, &pc)) {
             const bool notes = pc.notes();
             // the last piece's notes have been read; waited for at every piece, because a parity tells
             // only neighbouring phases apart
-            if (n > 0) ok = mbar_wait_bounded(&ctl.o_free, (n - 1) & 1, err);
-            if (notes && half == 0 && lane == 0) ctl.poison.n = 0;
-            ok = named_bar_and(2, 64, ok);
+            if (n > 0) ok = wait(&ctl.o_free, (n - 1) & 1, err);
+            ok = named_bar_and(10, 64, ok);
             int entry = 0;
+            uint32_t some = 0;
             const int LA = pc.two ? 1 : 2;
             item += min(LA, pc.nb);  // the first K blocks
             for (int k = 0; k < pc.nb && ok; ++k) {
@@ -605,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kb = pc.kb0 + k;
                 if (!pc.masked(a, kb)) continue;
                 // every masked block is waited for, in order, and the MMA of a block waits for its cleaning
-                ok = named_bar_and(2, 64, mbar_wait_bounded(&ctl.dirty[nd % kDirty], (nd / kDirty) & 1, err));
+                ok = named_bar_and(10, 64, wait(&ctl.dirty[nd % kDirty], (nd / kDirty) & 1, err));
                 if (!ok) break;
                 ++nd;
                 uint8_t* blk = smem + S::kOffRing + st * S::kBlock;
@@ -643,115 +812,142 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         found[i] = __reduce_or_sync(0xffffffffu, found[i]);
+                        some |= found[i];
                         if (lane == 0 && entry < kPoison) ctl.poison.keys[entry][2 * half + i] = found[i];
                     }
                     if (half == 0 && lane == 0 && entry < kPoison) ctl.poison.kb[entry] = kb;
                     ++entry;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads what was stored here
-                named_bar_sync(2, 64);
+                named_bar_sync(10, 64);
                 if (half == 0 && lane == 0) mbar_arrive(&ctl.full[st]);
             }
             if (half == 0 && lane == 0 && notes) ctl.poison.n = min(entry, kPoison);
+            if (lane == 0 && notes) ctl.poison.some[half] = some;
             __syncwarp();
             if (lane == 0 && notes) mbar_arrive(&ctl.clean_done);
             ++n;
         }
+    }
     } else {
         // ---------------------------------------------------------- softmax and epilogue
-        const int s = warp >> 2;               // sub-tile
-        const int r = (warp & 3) * 32 + lane;  // row of the sub-tile = TMEM lane
+        // two threads a row, each with half of the keys of a block and half of the columns of O
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHalves == 1 ? 208 : 104));
+        constexpr int NK = kKeys / kHalves, NC = NK / 32;  // keys of a thread
+        const int s = warp / kSubWarps, half = (warp % kSubWarps) >> 2;  // sub-tile, half
+        const int quad = warp & 3;                        // TMEM lanes 32 quad ..
+        const int r = quad * 32 + lane;                   // row of the sub-tile = TMEM lane
         const int tl = r / a.G, hh = r - tl * a.G;
-        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const uint32_t sa = tmem + s * kKeys + lane_off;
+        const uint32_t pair = 1 + s * 4 + quad;  // barrier of the warps of 32 rows
         const float sl2 = a.scale * kLog2e;
-        const bool cap = a.cap > 0.f;
-        const float k2 = cap ? 2.0f * kLog2e * a.scale / a.cap : 0.f, c_log2e = a.cap * kLog2e;
+        const float cap_k = CAP ? a.scale / a.cap : 0.f, c_log2e = a.cap * kLog2e;
         int noted = 0;        // pieces with notes so far
-        int cnt[2] = {0, 0};  // blocks of either sub-tile so far (phases of s_full and pv_done)
+        int cnt = 0, cnt_o = 0;  // blocks so far of this sub-tile, of the other (phases of s_full and pv_done)
         bool ok = true;
-        while (walk.next(a, &pc)) {
+        Piece nx;
+        bool more = walk.next(a, &nx);
+        while (more) {
+            pc = nx;
             const int tok = pc.two ? s * a.tps + tl : tl;  // token of the tile
             const bool valid = tl < a.tps && tok < pc.ntok;
             const int pos = pc.p0 + pc.t0 + tok;
             const int lo = a.window > 0 ? (int)max((long long)pos + 1 - a.window, 0ll) : 0;
-            int from[2], to[2];  // blocks of either sub-tile: from, from + step, .. < to
+            // blocks of this sub-tile: from, from + step, .. < to, and of the other (scalars: an array
+            // indexed by the sub-tile would live in local memory)
+            int from = s, to = pc.nb, from_o = s ^ 1, to_o = pc.nb;
             const int step = pc.two ? 1 : 2;
             if (pc.two) {
-                pc.range(a, 0, &from[0], &to[0]);
-                pc.range(a, 1, &from[1], &to[1]);
-            } else {
-                from[0] = 0;
-                from[1] = 1;
-                to[0] = to[1] = pc.nb;
+                pc.range(a, s, &from, &to);
+                pc.range(a, s ^ 1, &from_o, &to_o);
             }
+            const bool have = from < to, have_o = from_o < to_o;
+            if (have_o) cnt_o += (to_o - from_o + step - 1) / step;
             const int32_t* tab = a.table + (size_t)pc.b * a.max_pages;
-            auto page_ok = [&](int k) {  // whether the lane's page of block k lies in the pool
-                const int pi = (pc.kb0 + k) * (kKeys / kPage) + (lane & 7);
-                if (k >= to[s] || pi >= a.max_pages) return false;
+            auto page_ok = [&](int k) {  // whether the lane's page of this half of block k lies in the pool
+                const int pi = (pc.kb0 + k) * (kKeys / kPage) + (NK / kPage) * half + lane % (NK / kPage);
+                if (k >= to || pi >= a.max_pages) return false;
                 const int pg = tab[pi];
                 return pg >= 0 && pg < a.n_pages;
             };
-            bool pg = page_ok(from[s]);
+            bool pg = page_ok(from);
+            const bool busy = __any_sync(0xffffffffu, valid);
             float m = -INFINITY, l = 0.f;
-            for (int j = from[s]; j < to[s]; j += step) {
-                const uint32_t good = __ballot_sync(0xffffffffu, pg) & 0xffu;
+            for (int j = from; j < to; j += step) {
+                constexpr uint32_t kAll = (1u << (NK / kPage)) - 1;
+                const uint32_t good = __ballot_sync(0xffffffffu, pg) & kAll;
                 pg = page_ok(j + step);
-                const int key0 = (pc.kb0 + j) * kKeys;
-                const bool none = !valid || key0 > pos || key0 + kKeys - 1 < lo;
-                const bool whole = !none && key0 + kKeys - 1 <= pos && key0 >= lo && good == 0xffu;
-                if (ok && !mbar_wait_bounded(&ctl.s_full[s], cnt[s] & 1, err)) ok = false;
+                const int key0 = (pc.kb0 + j) * kKeys + NK * half;  // this thread's first key
+                // a row of nobody goes along unmasked: what it computes reaches no other row
+                const bool whole = !valid || (key0 + NK - 1 <= pos && key0 >= lo && good == kAll);
+                if (ok && !wait(&ctl.s_full[s], cnt & 1, err)) ok = false;
                 tc_fence_after();
-                uint32_t v[4][32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_issue(sa + 32 * c, v[c]);
-                tmem_ld_wait32(v[3]);
-                reg_fence32(v[0]);
-                reg_fence32(v[1]);
-                reg_fence32(v[2]);
-                if (cap) {
-                    if (a.cap <= 64.f) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int q = 0; q < 32; ++q)
-                                v[c][q] = __float_as_uint(capped(__uint_as_float(v[c][q]), k2, a.cap, c_log2e));
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int q = 0; q < 32; ++q)
-                                v[c][q] = __float_as_uint(capped_large(__uint_as_float(v[c][q]), a.scale, a.cap));
-                    }
+                if (!busy) {  // no row of this warp is anybody's: its P may stay what it is
+                    if (lane == 0) mbar_arrive(&ctl.p_full[s]);
+                    ++cnt;
+                    continue;
                 }
-                if (!whole) {
+                uint32_t v[NC][32];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < NC; ++c) tmem_ld32(sa + NK * half + 32 * c, v[c]);
+                tmem_ld_wait32(v[0]);
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) {
-                            const int key = key0 + 32 * c + q;
-                            if (none || key > pos || key < lo || !((good >> (2 * c + q / 16)) & 1))
-                                v[c][q] = __float_as_uint(-INFINITY);
-                        }
+                for (int c = 1; c < NC; ++c) reg_fence32(v[c]);
+                if (CAP) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            v[c][q] = __float_as_uint(capped(__uint_as_float(v[c][q]), cap_k, c_log2e));
+                }
+                const bool masked = __any_sync(0xffffffffu, !whole);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) {
+                        // bit q: the row sees key 32 c + q of this half (its keys are lo .. pos; pages may be missing)
+                        const int b0 = lo - key0 - 32 * c, b1 = pos - key0 - 32 * c;
+                        uint32_t see = b1 < 0 ? 0u : 0xffffffffu >> (31 - min(b1, 31));
+                        see &= b0 > 31 ? 0u : 0xffffffffu << max(b0, 0);
+                        see &= ((good >> (2 * c)) & 1 ? 0x0000ffffu : 0u) | ((good >> (2 * c)) & 2 ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q)
+                            if (!((see >> q) & 1)) v[c][q] = __float_as_uint(-INFINITY);
+                    }
                 }
                 float bm4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) bm4[q & 3] = fmaxf(bm4[q & 3], __uint_as_float(v[c][q]));
-                const float bm = fmaxf(fmaxf(bm4[0], bm4[1]), fmaxf(bm4[2], bm4[3])) * (cap ? 1.f : sl2);
-                const float mn = fmaxf(m, bm);
-                const bool grow = m != -INFINITY && mn > m + kRescale;
-                const float corr = grow ? ex2f(m - mn) : 1.f;
-                if (grow || m == -INFINITY) m = mn;
-                l *= corr;
+                    for (int q = 0; q < 32; ++q) bm4[q & 3] = max_nan(bm4[q & 3], __uint_as_float(v[c][q]));
+                float mn = max_nan(max_nan(bm4[0], bm4[1]), max_nan(bm4[2], bm4[3])) * (CAP ? 1.f : sl2);
+                // the two halves of a row agree on m: almost always neither has grown past it by 2^8 and it
+                // stays. Both warps have read their scores when this barrier opens, so P may go over them.
+                tc_fence_before();
+                float corr = 1.f;
+                bool grown = false;
+                const bool over = valid && !(mn <= m + kRescale);
+                if (kHalves == 1 ? __any_sync(0xffffffffu, over) : named_bar_or(pair, 64, over)) {
+                    if (kHalves == 2) {
+                        ctl.xm[s][half][r] = mn;
+                        named_bar_sync(pair, 64);
+                        mn = max_nan(mn, ctl.xm[s][half ^ 1][r]);
+                    }
+                    mn = max_nan(m, mn);
+                    if (!(mn < INFINITY)) mn = NAN;  // a score that is NaN or +inf makes the row NaN, from here on
+                    grown = valid && m != -INFINITY && mn > m + kRescale;
+                    if (grown) corr = ex2f(m - mn);
+                    if (grown || m == -INFINITY || mn != mn) m = mn;
+                    l *= corr;
+                }
+                tc_fence_after();
                 // P = 2^(S' - m), rounded to bf16, over the scores (keys 2i, 2i + 1 in column i)
-                const float2 mul2 = cap ? make_float2(1.f, 1.f) : make_float2(sl2, sl2);
+                const float2 mul2 = CAP ? make_float2(1.f, 1.f) : make_float2(sl2, sl2);
                 const float nm = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every score is -inf, 2^-inf = 0
                 const float2 nm2 = make_float2(nm, nm);
                 float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < NC; ++c) {
                     uint32_t ph[16];
 #pragma unroll
                     for (int q = 0; q < 32; q += 2) {
@@ -761,16 +957,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum2[(q >> 1) & 1] = fadd2(sum2[(q >> 1) & 1], p);
                         ph[q / 2] = pack_bf2(p.x, p.y);
                     }
-                    tmem_st16(sa + 16 * c, ph);
+                    tmem_st16(sa + (NK / 2) * half + 16 * c, ph);
                 }
                 l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
-                if (__any_sync(0xffffffffu, grow) && j > from[s]) {
-                    // O of the rows that grew, once the last block's product is in
-                    if (ok && !mbar_wait_bounded(&ctl.pv_done[s], (cnt[s] - 1) & 1, err)) ok = false;
+                if (__any_sync(0xffffffffu, grown) && j > from) {
+                    // O of the rows that grew (this half's columns), once the last block's product is in
+                    if (ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, err)) ok = false;
                     tc_fence_after();
-                    for (int c0 = 0; c0 < D; c0 += 32) {
+                    for (int c0 = half * (D / kHalves); c0 < (half + 1) * (D / kHalves); c0 += 32) {
                         uint32_t o[32];
-                        tmem_ld32_issue(tO + s * D + lane_off + c0, o);
+                        tmem_ld32(tO + s * D + lane_off + c0, o);
                         tmem_ld_wait32(o);
 #pragma unroll
                         for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * corr);
@@ -782,70 +978,73 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl.p_full[s]);
-                ++cnt[s];
-            }
-            {  // the other sub-tile's count
-                const int o = s ^ 1;
-                cnt[o] += from[o] < to[o] ? (to[o] - from[o] + step - 1) / step : 0;
+                ++cnt;
             }
 
-            // ---- epilogue
-            const bool have[2] = {from[0] < to[0], from[1] < to[1]};
-            if (have[s] && ok && !mbar_wait_bounded(&ctl.pv_done[s], (cnt[s] - 1) & 1, err)) ok = false;
-            float w[2] = {1.f, 1.f};  // weights of the two O's
-            if (!pc.two) {
-                if (have[s ^ 1] && ok && !mbar_wait_bounded(&ctl.pv_done[s ^ 1], (cnt[s ^ 1] - 1) & 1, err)) ok = false;
-                ctl.xch[s][r] = make_float2(m, l);
-                named_bar_sync(1, 256);
-                const float2 x = ctl.xch[0][r], y = ctl.xch[1][r];
-                m = fmaxf(x.x, y.x);
-                w[0] = x.x == -INFINITY ? 0.f : ex2f(x.x - m);
-                w[1] = y.x == -INFINITY ? 0.f : ex2f(y.x - m);
-                l = x.y * w[0] + y.y * w[1];
-                named_bar_sync(1, 256);
+            more = walk.next(a, &nx);  // while the last products are on their way
+
+            // ---- epilogue: l of the row, over both halves, and for a `one` tile over both sub-tiles
+            if (kHalves == 2) {
+                named_bar_sync(pair, 64);  // xm has been read
+                ctl.xm[s][half][r] = l;
+                named_bar_sync(pair, 64);
+                l = ctl.xm[s][0][r] + ctl.xm[s][1][r];
             }
+            float w0 = 1.f, w1 = 0.f;  // weights of this sub-tile's O, of the other's
+            if (!pc.two) {
+                if (kHalves == 2) named_bar_sync(pair, 64);
+                if (kHalves == 1 || half == 0) ctl.xm[s][0][r] = m;
+                if (kHalves == 1 || half == 1) ctl.xm[s][1][r] = l;
+                named_bar_sync(9, 32 * kSoftWarps);
+                const float mo = ctl.xm[s ^ 1][0][r], lo2 = ctl.xm[s ^ 1][1][r], ms = m;
+                named_bar_sync(9, 32 * kSoftWarps);
+                m = fmaxf(ms, mo);
+                w0 = ms == -INFINITY ? 0.f : ex2f(ms - m);
+                w1 = mo == -INFINITY ? 0.f : ex2f(mo - m);
+                // rounded alike in both sub-tiles' threads
+                l = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(lo2, w1));
+            }
+            if (have && ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, err)) ok = false;
+            if (!pc.two && have_o && ok && !wait(&ctl.pv_done[s ^ 1], (cnt_o - 1) & 1, err)) ok = false;
+            // an O that no block went into holds anything
+            const bool use = have && w0 != 0.f, use_o = !pc.two && have_o && w1 != 0.f;
             int poisoned = 0;
             if (pc.notes()) {
-                if (ok && !mbar_wait_bounded(&ctl.clean_done, noted & 1, err)) ok = false;
+                if (ok && !wait(&ctl.clean_done, noted & 1, err)) ok = false;
                 ++noted;
-                poisoned = ctl.poison.n;
+                if (ctl.poison.some[0] | ctl.poison.some[1]) poisoned = ctl.poison.n;
             }
             tc_fence_after();
-            // columns of this thread: all of its sub-tile's, or half of the joined result's
-            const int c_lo = pc.two ? 0 : s * (D / 2), c_hi = pc.two ? D : c_lo + D / 2;
+            // columns of this thread: its part of its sub-tile's, or of the joined result's
+            constexpr int kOwn = D / kHalves, kJoined = kOwn / 2;
+            const int c_lo = pc.two ? half * kOwn : (kHalves * s + half) * kJoined;
+            const int c_hi = c_lo + (pc.two ? kOwn : kJoined);
             const bool whole_tile = pc.starts && pc.ends;
             const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
-            uint16_t* dst = a.out + ((size_t)(pc.row0 + tok) * a.nq + (size_t)pc.g * a.G + hh) * D;
             float* slot = a.ws + (size_t)(2 * blockIdx.x + (pc.starts ? 1 : 0)) * S::kSlotFloats +
                           (pc.two ? s * S::kSubFloats : 0);
-            for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-                uint32_t o[32];
-                if (pc.two) {
-                    if (have[s]) {
-                        tmem_ld32_issue(tO + s * D + lane_off + c0, o);
-                        tmem_ld_wait32(o);
-                    } else {
+            // a warp's rows of the result pass through the place of Q: the sub-tile's own, done with, or for a
+            // joined result sub-tile 1's, not in use
+            const int cw = (c_hi - c_lo) / 8;  // 16-byte pieces of a row: 4, 8 or 16
+            uint4* stage = reinterpret_cast<uint4*>(smem + (pc.two ? s : 1) * S::kBlock) +
+                           (pc.two ? warp % kSubWarps : warp) * 32 * cw;
+#pragma unroll 1
+            for (int c0 = busy ? c_lo : c_hi; c0 < c_hi; c0 += 16) {
+                uint32_t o[16], o1[16];
+                tmem_ld16_issue(tO + s * D + lane_off + c0, o);
+                if (!pc.two) tmem_ld16_issue(tO + (s ^ 1) * D + lane_off + c0, o1);
+                tmem_ld_wait16(o);
+                reg_fence16(o1);
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = 0u;
-                    }
-                } else {
-                    tmem_ld32_issue(tO + lane_off + c0, o);  // sub-tile 0 has the first block of every piece
-                    tmem_ld_wait32(o);
-#pragma unroll
-                    for (int q = 0; q < 32; ++q)
-                        o[q] = w[0] == 0.f ? 0u : __float_as_uint(__uint_as_float(o[q]) * w[0]);
-                    if (have[1]) {
-                        uint32_t o1[32];
-                        tmem_ld32_issue(tO + D + lane_off + c0, o1);
-                        tmem_ld_wait32(o1);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            if (w[1] != 0.f)
-                                o[q] = __float_as_uint(fmaf(__uint_as_float(o1[q]), w[1], __uint_as_float(o[q])));
-                    }
+                for (int q = 0; q < 16; ++q) {
+                    float x = use ? __uint_as_float(o[q]) * w0 : 0.f;
+                    if (use_o) x = fmaf(__uint_as_float(o1[q]), w1, x);
+                    o[q] = __float_as_uint(x);
                 }
                 if (poisoned && valid) {
+#pragma unroll 1
                     for (int e = 0; e < poisoned; ++e)
+#pragma unroll 1
                         for (int i = 0; i < 4; ++i)
                             for (uint32_t bits = ctl.poison.keys[e][i]; bits; bits &= bits - 1) {
                                 const int key = ctl.poison.kb[e] * kKeys + 32 * i + __ffs(bits) - 1;
@@ -855,30 +1054,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint16_t* vr =
                                     a.v_pool + (((size_t)page * a.nkv + pc.g) * kPage + key % kPage) * D + c0;
 #pragma unroll
-                                for (int q = 0; q < 32; ++q) {
+                                for (int q = 0; q < 16; ++q) {
                                     const float x = bf2f(vr[q]);
                                     if (!(fabsf(x) < INFINITY)) o[q] = __float_as_uint(__uint_as_float(o[q]) + x);
                                 }
                             }
                 }
-                if (valid && ok) {
-                    if (whole_tile) {
+                if (whole_tile) {
+                    // 16-byte pieces, permuted within the row so that 8 lanes use all banks
 #pragma unroll
-                        for (int q = 0; q < 32; q += 8) {
-                            uint4 y;
-                            y.x = pack_bf2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv);
-                            y.y = pack_bf2(__uint_as_float(o[q + 2]) * inv, __uint_as_float(o[q + 3]) * inv);
-                            y.z = pack_bf2(__uint_as_float(o[q + 4]) * inv, __uint_as_float(o[q + 5]) * inv);
-                            y.w = pack_bf2(__uint_as_float(o[q + 6]) * inv, __uint_as_float(o[q + 7]) * inv);
-                            *reinterpret_cast<uint4*>(dst + c0 + q) = y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 32; q += 4)
-                            *reinterpret_cast<uint4*>(slot + ((size_t)((c0 + q) / 4) * kRows + r) * 4) =
-                                make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+                    for (int q = 0; q < 16; q += 8) {
+                        uint4 y;
+                        y.x = pack_bf2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv);
+                        y.y = pack_bf2(__uint_as_float(o[q + 2]) * inv, __uint_as_float(o[q + 3]) * inv);
+                        y.z = pack_bf2(__uint_as_float(o[q + 4]) * inv, __uint_as_float(o[q + 5]) * inv);
+                        y.w = pack_bf2(__uint_as_float(o[q + 6]) * inv, __uint_as_float(o[q + 7]) * inv);
+                        stage[lane * cw + (((c0 - c_lo + q) / 8) ^ (lane & (cw - 1)))] = y;
                     }
+                } else if (valid && ok) {
+#pragma unroll
+                    for (int q = 0; q < 16; q += 4)
+                        *reinterpret_cast<uint4*>(slot + ((size_t)((c0 + q) / 4) * kRows + r) * 4) =
+                            make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]);
                 }
+            }
+            if (whole_tile && busy) {
+                // the rows leave by whole segments: cw lanes a row
+                const long long at = valid && ok ? ((long long)(pc.row0 + tok) * a.nq + (long long)pc.g * a.G + hh) * D + c_lo : -1;
+                __syncwarp();
+#pragma unroll 4
+                for (int i = lane; i < 32 * cw; i += 32) {
+                    const int row = i / cw, c = i & (cw - 1);
+                    const long long to = __shfl_sync(0xffffffffu, at, row);
+                    if (to >= 0) *reinterpret_cast<uint4*>(a.out + to + 8 * c) = stage[row * cw + (c ^ (row & (cw - 1)))];
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next Q goes there by TMA
             }
             if (valid && ok && !whole_tile && c_lo == 0) {
                 slot[kRows * D + r] = m;
@@ -889,65 +1099,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&ctl.o_free);
         }
     }
-    // what the join needs to know of a tile that this run ends without having started it: the
-    // run's first piece
-    if (threadIdx.x == 0) {
-        Join jn{-1, 0, 0, 0};
-        Walk w2(a, run);
-        if (w2.next(a, &pc) && !pc.starts && pc.ends) jn = Join{run.first, pc.row0, pc.ntok, pc.g};
-        reinterpret_cast<Join*>(reinterpret_cast<char*>(a.ws) - kJoinBytes)[blockIdx.x] = jn;
-    }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == kSoftWarps + 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
 // Joins the pieces of the tile whose last piece is CTA blockIdx.x's first: with M the largest m,
-// O = sum 2^(m_i - M) O_i, l = sum 2^(m_i - M) l_i, in the order of the runs. A block takes 32 rows.
+// O = sum 2^(m_i - M) O_i, l = sum 2^(m_i - M) l_i, in the order of the runs. A block takes 32 rows;
+// the pieces' m and l are read all at once, into weights in shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkArgs a) {
     using S = Shape<D>;
+    __shared__ float wt[kCtas][32];  // m, then the weight 2^(m - M) / l of each piece and row
+    __shared__ float red[2][8][32];
+    const int last = blockIdx.x, part = blockIdx.y, sub = part >> 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const int last = blockIdx.x, part = blockIdx.y;
     const Join jn = reinterpret_cast<const Join*>(reinterpret_cast<const char*>(a.ws) - kJoinBytes)[last];
-    if (jn.first < 0) return;
-    const int sub = part >> 2, rows = 32 * (part & 3) + (threadIdx.x & 31);
-    const int tok = sub * a.tps + rows / a.G, hh = rows % a.G;
-    if (rows / a.G >= a.tps || tok >= jn.ntok) return;
-    auto piece = [&](int c) {  // a run's piece of the tile: the tail of the first, the head of the others
-        return a.ws + (size_t)(2 * c + (c == jn.first ? 1 : 0)) * S::kSlotFloats + sub * S::kSubFloats;
+    const int row = 32 * (part & 3) + lane, tl = row / a.G;
+    // the block's first row decides whether any of its rows is somebody's
+    if (jn.first < 0 || sub * a.tps + 32 * (part & 3) / a.G >= jn.ntok || 32 * (part & 3) / a.G >= a.tps) return;
+    const int tok = sub * a.tps + tl, hh = row - tl * a.G;
+    const bool valid = tl < a.tps && tok < jn.ntok;
+    const int np = last - jn.first + 1;
+    auto piece = [&](int i) {  // the tail of the first run, the head of the others
+        return a.ws + (size_t)(2 * (jn.first + i) + (i == 0 ? 1 : 0)) * S::kSlotFloats + sub * S::kSubFloats;
     };
     float M = -INFINITY;
-    for (int c = jn.first; c <= last; ++c) M = fmaxf(M, piece(c)[kRows * D + rows]);
-    float L = 0.f;
-    for (int c = jn.first; c <= last; ++c) {
-        const float* p = piece(c);
-        const float m = p[kRows * D + rows];
-        // a piece that saw nothing adds its l, 0 (NaN when every score was)
-        L += (m == -INFINITY ? 1.f : ex2f(m - M)) * p[kRows * D + kRows + rows];
+    for (int i = warp; i < np; i += 8) {
+        const float m = valid ? piece(i)[kRows * D + row] : -INFINITY;
+        wt[i][lane] = m;
+        M = fmaxf(M, m);
     }
+    red[0][warp][lane] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) M = fmaxf(M, red[0][w][lane]);
+    // a piece that saw nothing adds its l, 0 (NaN when every score was), and no O
+    float L = 0.f;
+    for (int i = warp; i < np; i += 8) {
+        const float m = wt[i][lane], l = valid ? piece(i)[kRows * D + kRows + row] : 0.f;
+        const float w = m == -INFINITY ? 0.f : ex2f(m - M);
+        wt[i][lane] = w;
+        L += m == -INFINITY ? l : w * l;
+    }
+    red[1][warp][lane] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) L += red[1][w][lane];
+    if (!valid) return;
     const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
     uint16_t* dst = a.out + ((size_t)(jn.row0 + tok) * a.nq + (size_t)jn.g * a.G + hh) * D;
-    for (int c4 = threadIdx.x >> 5; c4 < D / 4; c4 += 8) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = jn.first; c <= last; ++c) {
-            const float* p = piece(c);
-            const float m = p[kRows * D + rows];
-            if (m == -INFINITY) continue;
-            const float w = ex2f(m - M);
-            const float4 x = *reinterpret_cast<const float4*>(p + ((size_t)c4 * kRows + rows) * 4);
-            o.x = fmaf(w, x.x, o.x);
-            o.y = fmaf(w, x.y, o.y);
-            o.z = fmaf(w, x.z, o.z);
-            o.w = fmaf(w, x.w, o.w);
+    constexpr int C4 = D / 32;  // float4 columns a thread: warp, warp + 8, ..
+    float4 o[C4];
+#pragma unroll
+    for (int k = 0; k < C4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) {
+        const float w = wt[i][lane];
+        const float4* p = reinterpret_cast<const float4*>(piece(i)) + row;
+#pragma unroll
+        for (int k = 0; k < C4; ++k) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w != 0.f) x = p[(size_t)(warp + 8 * k) * kRows];  // a piece of weight 0 may hold anything
+            o[k].x = fmaf(w, x.x, o[k].x);
+            o[k].y = fmaf(w, x.y, o[k].y);
+            o[k].z = fmaf(w, x.z, o[k].z);
+            o[k].w = fmaf(w, x.w, o[k].w);
         }
+    }
+#pragma unroll
+    for (int k = 0; k < C4; ++k) {
         uint2 y;
-        y.x = pack_bf2(o.x * inv, o.y * inv);
-        y.y = pack_bf2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(dst + 4 * c4) = y;
+        y.x = pack_bf2(o[k].x * inv, o[k].y * inv);
+        y.y = pack_bf2(o[k].z * inv, o[k].w * inv);
+        *reinterpret_cast<uint2*>(dst + 4 * (warp + 8 * k)) = y;
     }
 }
 
@@ -977,9 +1207,10 @@ cudaError_t launch(const ChunkArgs& a, const void* q, int64_t ldq, const void* k
         if (e == cudaSuccess) e = tmap_bf16_sw128(&tmV, a.v_pool, 2, dims, strides, box);
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = ensure_smem(reinterpret_cast<const void*>(chunk_attn_kernel<D>), smem);
+    const auto kernel = a.cap > 0.f ? chunk_attn_kernel<D, true> : chunk_attn_kernel<D, false>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
-    chunk_attn_kernel<D><<<kCtas, kThreads, smem, st>>>(tmQ, tmK, tmV, a);
+    kernel<<<kCtas, kThreads, smem, st>>>(tmQ, tmK, tmV, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1016,11 +1247,11 @@ int chunk_split_check(const int32_t* cu, const int32_t* kv_len, int B, int T, in
         const Seq s = seq_of(a, b);
         long long n = 0;
         for (int t = 0; t < tile_count(a, s); ++t) {
-            if (blocks_before(a, s, t) != n) ++wrong;
+            if (units_before(a, s, t) != n) ++wrong;
             if (tile_blocks(a, s, t) < 1) ++wrong;
-            n += tile_blocks(a, s, t);
+            n += kTileCost + tile_blocks(a, s, t);
         }
-        if (seq_blocks(a, s) != n) ++wrong;
+        if (seq_units(a, s) != n) ++wrong;
         total += n * nkv;
     }
     // the tiles in order, walked beside the pieces
@@ -1039,13 +1270,12 @@ int chunk_split_check(const int32_t* cu, const int32_t* kv_len, int B, int T, in
         return true;
     };
     bool left = next_tile();
-    const long long runs = min((long long)kCtas, total);
-    for (int c = 0; c < runs; ++c) {
-        const Run run = run_from(a, 0, 0, c * total / runs, (c + 1) * total / runs, runs, total);
+    const Cut cut(total);
+    for (int c = 0; c < kCtas && cut.len(c) > 0; ++c) {
+        const Run run = run_from(a, 0, 0, cut, c);
         Walk w(a, run);
         Piece p;
         int pieces = 0;
-        long long len = 0;
         while (w.next(a, &p)) {
             if (!left) return wrong + 1;
             const Seq s = seq_of(a, b);
@@ -1061,11 +1291,9 @@ int chunk_split_check(const int32_t* cu, const int32_t* kv_len, int B, int T, in
                 for (int j = 0; j < p.nb; ++j)
                     if (p.p0 + p.t0 >= 0 && !(j >= from[0] && j < to[0]) && !(j >= from[1] && j < to[1])) ++wrong;
             off += p.nb;
-            len += p.nb;
             ++pieces;
             if (off == blocks) left = next_tile();
         }
-        if (len != run.len) ++wrong;
     }
     return left ? wrong + 1 : wrong;
 }

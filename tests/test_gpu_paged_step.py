@@ -298,6 +298,8 @@ def test_chunk_masked_places_hold_anything():
             dec.gqa_chunk_attn(q, kp, vp, ints(table), ints(cu), ints(lens), 128 ** -0.5, out)
             before, after = slice(0, 120), slice(120, 200)
             assert torch.equal(out[before], base[before]) and torch.equal(out[200:], base[200:])
+            if pool is kp and val != val:
+                assert torch.isnan(out[after]).all()
             if pool is vp:
                 assert (~torch.isfinite(out[after, :, 5])).all()
                 others = torch.arange(128, device="cuda") != 5
