@@ -9,7 +9,7 @@
 //
 // Tiles. The G query heads that share a kv head are packed with the tokens: a sub-tile is
 // 128 / G tokens x G heads = up to 128 MMA rows, a tile two sub-tiles (0 and 1), each with
-// eight softmax warps. Two ways to use the pair:
+// four softmax warps, a thread a row. Two ways to use the pair:
 //   two   the tile has rows for both: both read the same key blocks, so a K or V block is
 //         loaded once for 256 rows, and while one sub-tile's scores are being exponentiated
 //         the tensor cores work for the other;
@@ -36,8 +36,8 @@
 // memory, and where tokens of the tile see different keys, also take out values that are not
 // finite, note their keys, and the epilogue adds those values back to the rows that do see them.
 //
-// Warps: 0-7 and 8-15 softmax and epilogue of sub-tiles 0 and 1 (two threads a row, each half of
-// the keys), 16 TMA producer, 17 MMA issuer, 18-19 V cleaning. Shared memory: Q [2 sub-tiles][d / 64][128][64] and a ring of
+// Warps: 0-3 and 4-7 softmax and epilogue of sub-tiles 0 and 1, 8 TMA producer, 9 MMA issuer,
+// 10-11 V cleaning. Shared memory: Q [2 sub-tiles][d / 64][128][64] and a ring of
 // K and V blocks [d / 64][128][64] in the order of their use (all 128-byte swizzled).
 // TMEM columns: S/P of sub-tiles 0, 1 at 0, 128; O at 256, 256 + d.
 #include <cuda_runtime.h>
@@ -59,12 +59,14 @@ constexpr int kPage = 16;
 constexpr int kKeys = 128;     // keys of a block
 constexpr int kRows = 128;     // MMA rows of a sub-tile
 constexpr int kCtas = 148;     // runs the work is cut into: the SMs of a B200
-constexpr int kHalves = 1;      // threads a row of a sub-tile has (each takes 128 / kHalves keys of a block)
-constexpr int kSubWarps = 4 * kHalves;          // softmax warps of a sub-tile
+constexpr int kSubWarps = 4;    // softmax warps of a sub-tile, a thread a row
 constexpr int kSoftWarps = 2 * kSubWarps;
 constexpr int kThreads = 32 * (kSoftWarps + 4);  // softmax, TMA, MMA, two for cleaning V
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescale = 8.0f;  // log2 units
+// tanh(y) / y as a polynomial in y^2 <= 9/16 (relative minimax fit, off by 2^-20.8 at most)
+constexpr float kT0 = 0.999999463558197f, kT1 = -0.3332825005054474f, kT2 = 0.13258983194828033f,
+                kT3 = -0.05005630478262901f, kT4 = 0.01292963232845068f;
 constexpr int kDirty = 8;      // more than the V blocks a ring holds
 constexpr int kPoison = 8;     // masked blocks a tile can have: at most 3 on its diagonal and 3 at its window's edge
 
@@ -371,7 +373,7 @@ struct Control {
     Poison poison;
     union {
         long long scratch[64];
-        float xm[2][2][kRows];  // a block's maximum, at the end l, of each half of the rows
+        float2 ml[2][kRows];  // m and l of the two halves of a `one` tile
     };
 };
 
@@ -409,17 +411,6 @@ DEC_DEVINL bool wait(uint64_t* bar, uint32_t parity, int* err) {
         }
     }
     return true;
-}
-
-DEC_DEVINL bool named_bar_or(uint32_t id, uint32_t n, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(id), "r"(n)
-        : "memory");
-    return r != 0;
 }
 
 // tcgen05.ld of 32 columns without waiting.
@@ -487,22 +478,35 @@ DEC_DEVINL void commit_if(uint32_t on, uint64_t* bar) {
         : "memory");
 }
 DEC_DEVINL uint32_t desc_lo(uint32_t saddr, uint32_t leading) { return (saddr >> 4) | (leading << 16); }
+// The largest of three, NaN if any is.
+DEC_DEVINL float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+DEC_DEVINL float2 fmul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
 DEC_DEVINL float max_nan(float a, float b) {
     float d;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
     return d;
 }
 
-// The softcapped score c tanh(y) in log2 units, y = raw k: tanh(y) = 1 - 2 / (e^2y + 1), off by
-// some 2^-21, above |y| = 1/4, its Taylor series (next term 2^-18 of the value there) below, so
-// that the error stays a 2^-18 part of the score whatever the cap.
-DEC_DEVINL float capped(float raw, float k, float c_log2e) {
-    const float y = raw * k, y2 = y * y;
+// tanh(y) = 1 - 2 / (e^2y + 1), off by some 2^-21, above |y| = 1/4, its Taylor series (next term
+// 2^-18 of the value there) below, so that the error of c tanh(s / c) stays a 2^-18 part of the
+// score whatever the cap.
+DEC_DEVINL float tanh_exact(float y) {
+    const float y2 = y * y;
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2f(y * (2.0f * kLog2e)) + 1.0f));
     const float big = fmaf(-2.0f, r, 1.0f);
     const float small = y * fmaf(y2, fmaf(y2, fmaf(y2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.0f);
-    return c_log2e * (y2 < 0.0625f ? small : big);
+    return y2 < 0.0625f ? small : big;
 }
 
 template <int D, bool CAP>
@@ -553,10 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Run run = find_run(a, blockIdx.x, ctl.scratch);
     Walk walk(a, run);
     Piece pc;
-    // registers: 384 threads start with 168 each (640 with 96); 8 softmax warps x 208 + 4 x 88 (16 x 104 +
-    // 4 x 64) is as many
+    // 384 threads start with 168 registers each, 64512 in all: 8 softmax warps x 208 + 4 x 88 is as many
     if (warp >= kSoftWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kHalves == 1 ? 88 : 64));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kSoftWarps) {
         // ---------------------------------------------------------- TMA producer
         const int pool_rows = a.n_pages * a.nkv * kPage;
@@ -763,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the last piece's notes have been read; waited for at every piece, because a parity tells
             // only neighbouring phases apart
             if (n > 0) ok = wait(&ctl.o_free, (n - 1) & 1, err);
-            ok = named_bar_and(10, 64, ok);
+            ok = named_bar_and(2, 64, ok);
             int entry = 0;
             uint32_t some = 0;
             const int LA = pc.two ? 1 : 2;
@@ -774,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kb = pc.kb0 + k;
                 if (!pc.masked(a, kb)) continue;
                 // every masked block is waited for, in order, and the MMA of a block waits for its cleaning
-                ok = named_bar_and(10, 64, wait(&ctl.dirty[nd % kDirty], (nd / kDirty) & 1, err));
+                ok = named_bar_and(2, 64, wait(&ctl.dirty[nd % kDirty], (nd / kDirty) & 1, err));
                 if (!ok) break;
                 ++nd;
                 uint8_t* blk = smem + S::kOffRing + st * S::kBlock;
@@ -819,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++entry;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads what was stored here
-                named_bar_sync(10, 64);
+                named_bar_sync(2, 64);
                 if (half == 0 && lane == 0) mbar_arrive(&ctl.full[st]);
             }
             if (half == 0 && lane == 0 && notes) ctl.poison.n = min(entry, kPoison);
@@ -831,18 +834,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     } else {
         // ---------------------------------------------------------- softmax and epilogue
-        // two threads a row, each with half of the keys of a block and half of the columns of O
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHalves == 1 ? 208 : 104));
-        constexpr int NK = kKeys / kHalves, NC = NK / 32;  // keys of a thread
-        const int s = warp / kSubWarps, half = (warp % kSubWarps) >> 2;  // sub-tile, half
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        constexpr int NC = kKeys / 32;
+        const int s = warp / kSubWarps;                   // sub-tile
         const int quad = warp & 3;                        // TMEM lanes 32 quad ..
         const int r = quad * 32 + lane;                   // row of the sub-tile = TMEM lane
         const int tl = r / a.G, hh = r - tl * a.G;
         const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
         const uint32_t sa = tmem + s * kKeys + lane_off;
-        const uint32_t pair = 1 + s * 4 + quad;  // barrier of the warps of 32 rows
         const float sl2 = a.scale * kLog2e;
-        const float cap_k = CAP ? a.scale / a.cap : 0.f, c_log2e = a.cap * kLog2e;
+        const float cap_k = CAP ? a.scale / a.cap : 0.f, cap_raw = CAP ? a.cap / a.scale : 0.f;
         int noted = 0;        // pieces with notes so far
         int cnt = 0, cnt_o = 0;  // blocks so far of this sub-tile, of the other (phases of s_full and pv_done)
         bool ok = true;
@@ -865,8 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool have = from < to, have_o = from_o < to_o;
             if (have_o) cnt_o += (to_o - from_o + step - 1) / step;
             const int32_t* tab = a.table + (size_t)pc.b * a.max_pages;
-            auto page_ok = [&](int k) {  // whether the lane's page of this half of block k lies in the pool
-                const int pi = (pc.kb0 + k) * (kKeys / kPage) + (NK / kPage) * half + lane % (NK / kPage);
+            auto page_ok = [&](int k) {  // whether the lane's page of block k lies in the pool
+                const int pi = (pc.kb0 + k) * (kKeys / kPage) + lane % (kKeys / kPage);
                 if (k >= to || pi >= a.max_pages) return false;
                 const int pg = tab[pi];
                 return pg >= 0 && pg < a.n_pages;
@@ -875,12 +876,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool busy = __any_sync(0xffffffffu, valid);
             float m = -INFINITY, l = 0.f;
             for (int j = from; j < to; j += step) {
-                constexpr uint32_t kAll = (1u << (NK / kPage)) - 1;
+                constexpr uint32_t kAll = (1u << (kKeys / kPage)) - 1;
                 const uint32_t good = __ballot_sync(0xffffffffu, pg) & kAll;
                 pg = page_ok(j + step);
-                const int key0 = (pc.kb0 + j) * kKeys + NK * half;  // this thread's first key
+                const int key0 = (pc.kb0 + j) * kKeys;
                 // a row of nobody goes along unmasked: what it computes reaches no other row
-                const bool whole = !valid || (key0 + NK - 1 <= pos && key0 >= lo && good == kAll);
+                const bool whole = !valid || (key0 + kKeys - 1 <= pos && key0 >= lo && good == kAll);
                 if (ok && !wait(&ctl.s_full[s], cnt & 1, err)) ok = false;
                 tc_fence_after();
                 if (!busy) {  // no row of this warp is anybody's: its P may stay what it is
@@ -890,22 +891,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint32_t v[NC][32];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) tmem_ld32(sa + NK * half + 32 * c, v[c]);
+                for (int c = 0; c < NC; ++c) tmem_ld32(sa + 32 * c, v[c]);
                 tmem_ld_wait32(v[0]);
 #pragma unroll
                 for (int c = 1; c < NC; ++c) reg_fence32(v[c]);
                 if (CAP) {
+                    // in units of the raw score: raw tanh(y) / y, y = raw scale / cap, by a polynomial in y^2 where no
+                    // |y| is above 3/4 (in practice nowhere), packed two by two; else one by one from scores read again
+                    const float2 k2 = make_float2(cap_k * cap_k, cap_k * cap_k);
+                    float tm4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
 #pragma unroll
-                        for (int q = 0; q < 32; ++q)
-                            v[c][q] = __float_as_uint(capped(__uint_as_float(v[c][q]), cap_k, c_log2e));
+                        for (int q = 0; q < 32; q += 2) {
+                            const float2 x = make_float2(__uint_as_float(v[c][q]), __uint_as_float(v[c][q + 1]));
+                            const float2 t = fmul2(fmul2(x, k2), x);
+                            tm4[(q >> 1) & 3] = max3_nan(tm4[(q >> 1) & 3], t.x, t.y);
+                            float2 u = ffma2(t, make_float2(kT4, kT4), make_float2(kT3, kT3));
+                            u = ffma2(u, t, make_float2(kT2, kT2));
+                            u = ffma2(u, t, make_float2(kT1, kT1));
+                            u = fmul2(ffma2(u, t, make_float2(kT0, kT0)), x);
+                            v[c][q] = __float_as_uint(u.x);
+                            v[c][q + 1] = __float_as_uint(u.y);
+                        }
+                    const float tmx = max_nan(max_nan(tm4[0], tm4[1]), max_nan(tm4[2], tm4[3]));
+                    if (__any_sync(0xffffffffu, !(tmx <= 0.5625f))) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(sa + c0, x);
+                            tmem_ld_wait32(x);
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) x[q] = __float_as_uint(cap_raw * tanh_exact(__uint_as_float(x[q]) * cap_k));
+                            tmem_st16(sa + c0, x);
+                            tmem_st16(sa + c0 + 16, x + 16);
+                        }
+                        tmem_st_wait();
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) tmem_ld32(sa + 32 * c, v[c]);
+                        tmem_ld_wait32(v[0]);
+#pragma unroll
+                        for (int c = 1; c < NC; ++c) reg_fence32(v[c]);
+                    }
                 }
                 const bool masked = __any_sync(0xffffffffu, !whole);
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        // bit q: the row sees key 32 c + q of this half (its keys are lo .. pos; pages may be missing)
+                        // bit q: the row sees key 32 c + q of these (its keys are lo .. pos; pages may be missing)
                         const int b0 = lo - key0 - 32 * c, b1 = pos - key0 - 32 * c;
                         uint32_t see = b1 < 0 ? 0u : 0xffffffffu >> (31 - min(b1, 31));
                         see &= b0 > 31 ? 0u : 0xffffffffu << max(b0, 0);
@@ -919,30 +952,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) bm4[q & 3] = max_nan(bm4[q & 3], __uint_as_float(v[c][q]));
-                float mn = max_nan(max_nan(bm4[0], bm4[1]), max_nan(bm4[2], bm4[3])) * (CAP ? 1.f : sl2);
-                // the two halves of a row agree on m: almost always neither has grown past it by 2^8 and it
-                // stays. Both warps have read their scores when this barrier opens, so P may go over them.
-                tc_fence_before();
-                float corr = 1.f;
-                bool grown = false;
+                    for (int q = 0; q < 32; q += 2)
+                        bm4[(q >> 1) & 3] =
+                            max3_nan(bm4[(q >> 1) & 3], __uint_as_float(v[c][q]), __uint_as_float(v[c][q + 1]));
+                float mn = max_nan(max_nan(bm4[0], bm4[1]), max_nan(bm4[2], bm4[3])) * sl2;
+                // almost always no row has grown past its m by 2^8, and m stays
                 const bool over = valid && !(mn <= m + kRescale);
-                if (kHalves == 1 ? __any_sync(0xffffffffu, over) : named_bar_or(pair, 64, over)) {
-                    if (kHalves == 2) {
-                        ctl.xm[s][half][r] = mn;
-                        named_bar_sync(pair, 64);
-                        mn = max_nan(mn, ctl.xm[s][half ^ 1][r]);
-                    }
+                if (__any_sync(0xffffffffu, over)) {
                     mn = max_nan(m, mn);
                     if (!(mn < INFINITY)) mn = NAN;  // a score that is NaN or +inf makes the row NaN, from here on
-                    grown = valid && m != -INFINITY && mn > m + kRescale;
-                    if (grown) corr = ex2f(m - mn);
+                    const bool grown = valid && m != -INFINITY && mn > m + kRescale;
+                    const float corr = grown ? ex2f(m - mn) : 1.f;
                     if (grown || m == -INFINITY || mn != mn) m = mn;
                     l *= corr;
+                    if (__any_sync(0xffffffffu, grown) && j > from) {
+                        // O of the rows that grew, once the last block's product is in
+                        if (ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, err)) ok = false;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_issue(tO + s * D + lane_off + c0, o);
+                            tmem_ld_wait16(o);
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * corr);
+                            tmem_st16(tO + s * D + lane_off + c0, o);
+                        }
+                    }
                 }
-                tc_fence_after();
-                // P = 2^(S' - m), rounded to bf16, over the scores (keys 2i, 2i + 1 in column i)
-                const float2 mul2 = CAP ? make_float2(1.f, 1.f) : make_float2(sl2, sl2);
+                // P = 2^(S' - m), rounded to bf16, over the scores (keys 2i, 2i + 1 in column i).
+                const float2 mul2 = make_float2(sl2, sl2);
                 const float nm = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every score is -inf, 2^-inf = 0
                 const float2 nm2 = make_float2(nm, nm);
                 float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -957,23 +996,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum2[(q >> 1) & 1] = fadd2(sum2[(q >> 1) & 1], p);
                         ph[q / 2] = pack_bf2(p.x, p.y);
                     }
-                    tmem_st16(sa + (NK / 2) * half + 16 * c, ph);
+                    tmem_st16(sa + 16 * c, ph);
                 }
                 l += (sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y);
-                if (__any_sync(0xffffffffu, grown) && j > from) {
-                    // O of the rows that grew (this half's columns), once the last block's product is in
-                    if (ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, err)) ok = false;
-                    tc_fence_after();
-                    for (int c0 = half * (D / kHalves); c0 < (half + 1) * (D / kHalves); c0 += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + s * D + lane_off + c0, o);
-                        tmem_ld_wait32(o);
-#pragma unroll
-                        for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * corr);
-                        tmem_st16(tO + s * D + lane_off + c0, o);
-                        tmem_st16(tO + s * D + lane_off + c0 + 16, o + 16);
-                    }
-                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -983,21 +1008,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             more = walk.next(a, &nx);  // while the last products are on their way
 
-            // ---- epilogue: l of the row, over both halves, and for a `one` tile over both sub-tiles
-            if (kHalves == 2) {
-                named_bar_sync(pair, 64);  // xm has been read
-                ctl.xm[s][half][r] = l;
-                named_bar_sync(pair, 64);
-                l = ctl.xm[s][0][r] + ctl.xm[s][1][r];
-            }
+            // ---- epilogue: m and l of a `one` tile, over both sub-tiles
             float w0 = 1.f, w1 = 0.f;  // weights of this sub-tile's O, of the other's
             if (!pc.two) {
-                if (kHalves == 2) named_bar_sync(pair, 64);
-                if (kHalves == 1 || half == 0) ctl.xm[s][0][r] = m;
-                if (kHalves == 1 || half == 1) ctl.xm[s][1][r] = l;
-                named_bar_sync(9, 32 * kSoftWarps);
-                const float mo = ctl.xm[s ^ 1][0][r], lo2 = ctl.xm[s ^ 1][1][r], ms = m;
-                named_bar_sync(9, 32 * kSoftWarps);
+                ctl.ml[s][r] = make_float2(m, l);
+                named_bar_sync(1, 32 * kSoftWarps);
+                const float mo = ctl.ml[s ^ 1][r].x, lo2 = ctl.ml[s ^ 1][r].y, ms = m;
+                named_bar_sync(1, 32 * kSoftWarps);
                 m = fmaxf(ms, mo);
                 w0 = ms == -INFINITY ? 0.f : ex2f(ms - m);
                 w1 = mo == -INFINITY ? 0.f : ex2f(mo - m);
@@ -1015,10 +1032,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ctl.poison.some[0] | ctl.poison.some[1]) poisoned = ctl.poison.n;
             }
             tc_fence_after();
-            // columns of this thread: its part of its sub-tile's, or of the joined result's
-            constexpr int kOwn = D / kHalves, kJoined = kOwn / 2;
-            const int c_lo = pc.two ? half * kOwn : (kHalves * s + half) * kJoined;
-            const int c_hi = c_lo + (pc.two ? kOwn : kJoined);
+            // columns of this thread: its sub-tile's, or half of the joined result's
+            const int c_lo = pc.two ? 0 : s * (D / 2), c_hi = pc.two ? D : c_lo + D / 2;
             const bool whole_tile = pc.starts && pc.ends;
             const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
             float* slot = a.ws + (size_t)(2 * blockIdx.x + (pc.starts ? 1 : 0)) * S::kSlotFloats +
