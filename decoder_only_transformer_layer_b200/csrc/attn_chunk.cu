@@ -67,6 +67,10 @@ constexpr float kRescale = 8.0f;  // log2 units
 // tanh(y) / y as a polynomial in y^2 <= 9/16 (relative minimax fit, off by 2^-20.8 at most)
 constexpr float kT0 = 0.999999463558197f, kT1 = -0.3332825005054474f, kT2 = 0.13258983194828033f,
                 kT3 = -0.05005630478262901f, kT4 = 0.01292963232845068f;
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
 constexpr int kDirty = 8;      // more than the V blocks a ring holds
 constexpr int kPoison = 8;     // masked blocks a tile can have: at most 3 on its diagonal and 3 at its window's edge
 
@@ -1123,77 +1127,109 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the tile whose last piece is CTA blockIdx.x's first: with M the largest m,
-// O = sum 2^(m_i - M) O_i, l = sum 2^(m_i - M) l_i, in the order of the runs. A block takes 32 rows;
-// the pieces' m and l are read all at once, into weights in shared memory.
+// O = sum 2^(m_i - M) O_i, l = sum 2^(m_i - M) l_i, in the order of the runs. Eight blocks share a tile:
+// first by groups of 32 rows, then, where it has fewer than eight, by columns (a decode's tile has one
+// group and many pieces, a prompt's eight and two). The pieces' m and l are read all at once, into
+// weights in shared memory. Latency is the bound: three dependent reads of what other SMs have just
+// written.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinBlocks = 8;
+
 template <int D>
-__global__ void __launch_bounds__(256) chunk_join_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const ChunkArgs a) {
     using S = Shape<D>;
-    __shared__ float wt[kCtas][32];  // m, then the weight 2^(m - M) / l of each piece and row
-    __shared__ float red[2][8][32];
-    const int last = blockIdx.x, part = blockIdx.y, sub = part >> 2;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // of each piece and row: m, then the weight 2^(m - M); and l (two arrays of 18.5 KB)
+    __shared__ float wt[kCtas][32], wl[kCtas][32];
+    __shared__ float red[2][kJoinWarps][32];
+    const int last = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const Join jn = reinterpret_cast<const Join*>(reinterpret_cast<const char*>(a.ws) - kJoinBytes)[last];
-    const int row = 32 * (part & 3) + lane, tl = row / a.G;
-    // the block's first row decides whether any of its rows is somebody's
-    if (jn.first < 0 || sub * a.tps + 32 * (part & 3) / a.G >= jn.ntok || 32 * (part & 3) / a.G >= a.tps) return;
-    const int tok = sub * a.tps + tl, hh = row - tl * a.G;
-    const bool valid = tl < a.tps && tok < jn.ntok;
+    if (jn.first < 0) return;
     const int np = last - jn.first + 1;
+    const int groups0 = (min(jn.ntok, a.tps) * a.G + 31) / 32, groups1 = (max(jn.ntok - a.tps, 0) * a.G + 31) / 32;
+    int sharing = kJoinBlocks;  // blocks of a group of rows
+    while (sharing > 1 && sharing * (groups0 + groups1) > kJoinBlocks) sharing >>= 1;
+    const int group = blockIdx.y / sharing, share = blockIdx.y % sharing;
+    if (group >= groups0 + groups1) return;
+    const int sub = group >= groups0, row = 32 * (group - (sub ? groups0 : 0)) + lane;
+    const int tl = row / a.G, hh = row - tl * a.G, tok = sub * a.tps + tl;
+    const bool valid = tl < a.tps && tok < jn.ntok;
     auto piece = [&](int i) {  // the tail of the first run, the head of the others
         return a.ws + (size_t)(2 * (jn.first + i) + (i == 0 ? 1 : 0)) * S::kSlotFloats + sub * S::kSubFloats;
     };
     float M = -INFINITY;
-    for (int i = warp; i < np; i += 8) {
-        const float m = valid ? piece(i)[kRows * D + row] : -INFINITY;
+    for (int i = warp; i < np; i += kJoinWarps) {
+        const float* p = piece(i) + kRows * D + row;
+        const float m = valid ? p[0] : -INFINITY;
+        wl[i][lane] = valid ? p[kRows] : 0.f;
         wt[i][lane] = m;
         M = fmaxf(M, m);
     }
     red[0][warp][lane] = M;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, red[0][w][lane]);
+    for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, red[0][w][lane]);
     // a piece that saw nothing adds its l, 0 (NaN when every score was), and no O
     float L = 0.f;
-    for (int i = warp; i < np; i += 8) {
-        const float m = wt[i][lane], l = valid ? piece(i)[kRows * D + kRows + row] : 0.f;
-        const float w = m == -INFINITY ? 0.f : ex2f(m - M);
+    for (int i = warp; i < np; i += kJoinWarps) {
+        const float m = wt[i][lane], w = m == -INFINITY ? 0.f : ex2f(m - M);
         wt[i][lane] = w;
-        L += m == -INFINITY ? l : w * l;
+        L += m == -INFINITY ? wl[i][lane] : w * wl[i][lane];
     }
     red[1][warp][lane] = L;
     __syncthreads();
     L = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) L += red[1][w][lane];
+    for (int w = 0; w < kJoinWarps; ++w) L += red[1][w][lane];
     if (!valid) return;
     const float inv = L > 0.f || L != L ? 1.0f / L : 0.f;
     uint16_t* dst = a.out + ((size_t)(jn.row0 + tok) * a.nq + (size_t)jn.g * a.G + hh) * D;
-    constexpr int C4 = D / 32;  // float4 columns a thread: warp, warp + 8, ..
-    float4 o[C4];
+    const int cols = D / 4 / sharing;  // float4 columns of this block
+    // KC columns (warp, warp + 8, ..) of KP pieces at once, none of the loads behind a test of its weight: one
+    // after the other they took 34 us for 18 pieces. A piece of weight 0 holds finite values (or its
+    // row is not finite anyway); past the last piece the last one is read again, and not used.
+    auto columns = [&](auto kc, auto kp, int c0) {
+        constexpr int KC = decltype(kc)::value, KP = decltype(kp)::value;
+        const size_t at = ((size_t)c0 * kRows + row) * 4;
+        float4 o[KC];
 #pragma unroll
-    for (int k = 0; k < C4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < np; ++i) {
-        const float w = wt[i][lane];
-        const float4* p = reinterpret_cast<const float4*>(piece(i)) + row;
+        for (int k = 0; k < KC; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < np; i0 += KP) {
+            float4 x[KP][KC];
 #pragma unroll
-        for (int k = 0; k < C4; ++k) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (w != 0.f) x = p[(size_t)(warp + 8 * k) * kRows];  // a piece of weight 0 may hold anything
-            o[k].x = fmaf(w, x.x, o[k].x);
-            o[k].y = fmaf(w, x.y, o[k].y);
-            o[k].z = fmaf(w, x.z, o[k].z);
-            o[k].w = fmaf(w, x.w, o[k].w);
+            for (int u = 0; u < KP; ++u) {
+                const float* p = piece(min(i0 + u, np - 1)) + at;
+#pragma unroll
+                for (int k = 0; k < KC; ++k)
+                    x[u][k] = __ldcg(reinterpret_cast<const float4*>(p + (size_t)k * kJoinWarps * kRows * 4));
+            }
+#pragma unroll
+            for (int u = 0; u < KP; ++u)
+                if (i0 + u < np) {
+                    const float w = wt[i0 + u][lane];
+#pragma unroll
+                    for (int k = 0; k < KC; ++k) {
+                        o[k].x = fmaf(w, x[u][k].x, o[k].x);
+                        o[k].y = fmaf(w, x[u][k].y, o[k].y);
+                        o[k].z = fmaf(w, x[u][k].z, o[k].z);
+                        o[k].w = fmaf(w, x[u][k].w, o[k].w);
+                    }
+                }
         }
-    }
 #pragma unroll
-    for (int k = 0; k < C4; ++k) {
-        uint2 y;
-        y.x = pack_bf2(o[k].x * inv, o[k].y * inv);
-        y.y = pack_bf2(o[k].z * inv, o[k].w * inv);
-        *reinterpret_cast<uint2*>(dst + 4 * (warp + 8 * k)) = y;
-    }
+        for (int k = 0; k < KC; ++k) {
+            uint2 y;
+            y.x = pack_bf2(o[k].x * inv, o[k].y * inv);
+            y.y = pack_bf2(o[k].z * inv, o[k].w * inv);
+            *reinterpret_cast<uint2*>(dst + 4 * (c0 + kJoinWarps * k)) = y;
+        }
+    };
+    const int c0 = share * cols + warp;
+    if (cols == 4 * kJoinWarps)
+        columns(Int<4>(), Int<2>(), c0);
+    else if (cols == 2 * kJoinWarps)
+        columns(Int<2>(), Int<4>(), c0);
+    else if (warp < cols)
+        columns(Int<1>(), Int<8>(), c0);
 }
 
 template <int D>
@@ -1229,8 +1265,8 @@ cudaError_t launch(const ChunkArgs& a, const void* q, int64_t ldq, const void* k
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCtas, 8);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(kCtas, kJoinBlocks);
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -20,6 +20,8 @@
 #include <stdint.h>
 
 #include <exception>
+#include <mutex>
+#include <set>
 #include <string>
 
 #include "../../include/dec_api.h"
@@ -34,7 +36,7 @@ dec_status bad(dec_status s, const std::string& why) {
     return s;
 }
 
-struct Stat {  // a piece of a row: max, sum of e^((l - max) / T), argmax
+struct Stat {  // a piece of a row: max, sum of e^((l - max) / T) (0 in a greedy sequence), argmax (greedy only)
     float m, s;
     int arg, pad;
 };
@@ -55,59 +57,140 @@ struct VerifyArgs {
     int32_t* tokens;         // [B][n + 1]
 };
 
+constexpr int kMaxDrafts = 64;
+
 DEC_DEVINL int drafts_of(const VerifyArgs& a, int b) {
     return a.count ? min(max(a.count[b], 0), a.n) : a.n;
 }
 
-constexpr int kStatThreads = 256;
+// log2(e) / T; a temperature so small that it overflows is a temperature of 1e-30
+DEC_DEVINL float log2e_over(float T) { return T > 0.f ? fminf(1.4426950408889634f / T, 1e30f) : 0.f; }
 
-// One piece of one row.
+DEC_DEVINL float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr int kStatThreads = 256;
+constexpr int kBatch = 4;  // 16-byte loads a thread has in flight
+
+// x joined to y, of pieces in this order: the first largest value keeps its index.
+DEC_DEVINL Stat join(const Stat& x, const Stat& y, float k) {
+    Stat z;
+    z.m = fmaxf(x.m, y.m);
+    z.s = z.m == -INFINITY ? 0.f : x.s * ex2f((x.m - z.m) * k) + y.s * ex2f((y.m - z.m) * k);
+    z.arg = x.m > y.m || (x.m == y.m && x.arg < y.arg) ? x.arg : y.arg;
+    z.pad = 0;
+    return z;
+}
+
+// One piece of one row. A thread takes 16-byte vectors (the row's first and last values one by
+// one, where it does not begin or end on a vector), four at a time, with one move of its maximum
+// for the four.
 __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(VerifyArgs a) {
-    const int b = blockIdx.y / (2 * a.n + 1), i = blockIdx.y % (2 * a.n + 1);
+    pdl_trigger();
+    const int rows = 2 * a.n + 1;
+    const int b = blockIdx.y / rows, i = blockIdx.y - b * rows;
     const int nb = drafts_of(a, b);
     const float T = a.temp ? a.temp[b] : 1.f;
-    const bool dr = i > a.n;
-    if (dr ? (!a.draft || T <= 0.f || i - a.n - 1 >= nb) : i > nb) return;
+    const bool dr = i > a.n, warm = T > 0.f;
+    if (dr ? (!a.draft || !warm || i - a.n - 1 >= nb) : i > nb) return;
     const float* row = dr ? a.draft + b * a.d_seq + (i - a.n - 1) * a.d_row : a.target + b * a.t_seq + i * a.t_row;
     const int lo = blockIdx.x * a.piece, hi = min(a.V, lo + a.piece);
-    const float k = T > 0.f ? 1.4426950408889634f / T : 0.f;
-    float m = -INFINITY, s = 0.f;
-    int arg = 0x7fffffff;
-    for (int j = lo + threadIdx.x; j < hi; j += kStatThreads) {
-        const float l = row[j];
-        if (l > m) {
-            s *= exp2f((m - l) * k);
-            m = l;
-            arg = j;
+    const float k = log2e_over(T);
+    Stat st{-INFINITY, 0.f, 0x7fffffff, 0};
+    auto one = [&](float l, int j) {
+        const float mn = fmaxf(st.m, l);
+        if (warm)
+            st.s = mn == -INFINITY ? 0.f : st.s * ex2f((st.m - mn) * k) + ex2f((l - mn) * k);
+        else if (l > st.m)
+            st.arg = j;
+        st.m = mn;
+    };
+    // vectors v0 .. v1 - 1 from `base`, the first 16-byte boundary at or after lo
+    const int skip = min((int)((16 - ((uintptr_t)(row + lo) & 15)) & 15) / 4, hi - lo);
+    const int base = lo + skip, nv = (hi - base) / 4;
+    if (threadIdx.x < skip) one(row[lo + threadIdx.x], lo + threadIdx.x);
+    const float4* vec = reinterpret_cast<const float4*>(row + base);
+    for (int v0 = threadIdx.x; v0 < nv; v0 += kStatThreads * kBatch) {
+        float4 x[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int v = v0 + q * kStatThreads;
+            x[q] = v < nv ? __ldcs(vec + v) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         }
-        if (m > -INFINITY) s += exp2f((l - m) * k);
+        float mn = st.m;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) mn = fmaxf(mn, fmaxf(fmaxf(x[q].x, x[q].y), fmaxf(x[q].z, x[q].w)));
+        if (warm) {
+            if (mn == -INFINITY) continue;
+            float s0 = st.s * ex2f((st.m - mn) * k), s1 = 0.f;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                s0 += ex2f((x[q].x - mn) * k) + ex2f((x[q].y - mn) * k);
+                s1 += ex2f((x[q].z - mn) * k) + ex2f((x[q].w - mn) * k);
+            }
+            st.s = s0 + s1;
+        } else if (mn > st.m) {
+#pragma unroll
+            for (int q = kBatch - 1; q >= 0; --q) {  // ends at the first place of the largest value
+                const int j = base + 4 * (v0 + q * kStatThreads);
+                if (x[q].w == mn) st.arg = j + 3;
+                if (x[q].z == mn) st.arg = j + 2;
+                if (x[q].y == mn) st.arg = j + 1;
+                if (x[q].x == mn) st.arg = j;
+            }
+        }
+        st.m = mn;
     }
-    __shared__ Stat sh[kStatThreads];
-    sh[threadIdx.x] = Stat{m, s, arg, 0};
+    for (int j = base + 4 * nv + threadIdx.x; j < hi; j += kStatThreads) one(row[j], j);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Stat y;
+        y.m = __shfl_down_sync(0xffffffffu, st.m, o);
+        y.s = __shfl_down_sync(0xffffffffu, st.s, o);
+        y.arg = __shfl_down_sync(0xffffffffu, st.arg, o);
+        st = join(st, y, k);
+    }
+    __shared__ Stat sh[kStatThreads / 32];
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = st;
     __syncthreads();
-    for (int o = kStatThreads / 2; o > 0; o >>= 1) {
-        if (threadIdx.x < o) {
-            const Stat x = sh[threadIdx.x], y = sh[threadIdx.x + o];
-            Stat z;
-            z.m = fmaxf(x.m, y.m);
-            z.s = z.m == -INFINITY ? 0.f : x.s * exp2f((x.m - z.m) * k) + y.s * exp2f((y.m - z.m) * k);
-            z.arg = x.m > y.m || (x.m == y.m && x.arg < y.arg) ? x.arg : y.arg;
-            z.pad = 0;
-            sh[threadIdx.x] = z;
-        }
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kStatThreads / 32; ++w) st = join(st, sh[w], k);
+        a.stats[(size_t)blockIdx.y * a.splits + blockIdx.x] = st;
     }
-    if (threadIdx.x == 0) a.stats[(size_t)blockIdx.y * a.splits + blockIdx.x] = sh[0];
 }
 
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kPickMaxCluster = 8;
+constexpr int kPickCluster = 16;  // most CTAs of a sequence
+
+// 2^x in fp64 for x <= 0, to some 2^-50: x = n + i / 64 + f with |f| <= 1/128, 2^(i / 64) from a
+// table, the exponential series of f ln 2 up to the 5th power (the next term is below 2^-54), n into
+// the exponent. Below 2^-1000 it is 0, which no sum of at most 2^30 terms with a term of 1 among
+// them can tell. 10 fp64 operations; the series alone took 18, and fp64 is what bounds the draw.
+DEC_DEVINL double exp2_d(double x, const double* table) {
+    constexpr double kLn2 = 0.69314718055994530942, kMagic = 105553116266496.0;  // 1.5 x 2^46: steps of 1/64
+    const double t = x + kMagic;
+    const double f = x - (t - kMagic);
+    double p = kLn2 * kLn2 * kLn2 * kLn2 * kLn2 / 120.0;
+    p = fma(p, f, kLn2 * kLn2 * kLn2 * kLn2 / 24.0);
+    p = fma(p, f, kLn2 * kLn2 * kLn2 / 6.0);
+    p = fma(p, f, kLn2 * kLn2 / 2.0);
+    p = fma(p, f, kLn2);
+    p = fma(p, f, 1.0);
+    const int n = __double2loint(t);
+    p *= table[n & 63];
+    return x > -1000.0 ? __hiloint2double(__double2hiint(p) + ((n >> 6) << 20), __double2loint(p)) : 0.0;
+}
 
 struct PickShared {
-    Stat row[1];
+    Stat row[2 * kMaxDrafts + 1];
+    int verdict[kMaxDrafts];         // of each draft: 1 accepted, 0 not, 2 too close for fp32 sums
     double warp[2][kPickWarps];
-    double cta[2][kPickMaxCluster];  // written by every CTA of the cluster
+    double cta[2][kPickCluster];     // written by every CTA of the cluster
+    double table[64];                // 2^(i / 64)
 };
 
 DEC_DEVINL double warp_sum_d(double v) {
@@ -117,7 +200,7 @@ DEC_DEVINL double warp_sum_d(double v) {
 }
 
 // The sums over the cluster of x and y (one value a thread), in a fixed order; also this
-// CTA's own totals in sh.cta. Every thread of the cluster calls it.
+// CTA's own warps' totals in sh.warp and every CTA's in sh.cta. Every thread of the cluster calls it.
 DEC_DEVINL double2 cluster_sum(PickShared& sh, double x, double y, int rank, int C) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     x = warp_sum_d(x);
@@ -128,12 +211,11 @@ DEC_DEVINL double2 cluster_sum(PickShared& sh, double x, double y, int rank, int
         sh.warp[1][warp] = y;
     }
     __syncthreads();
-    if (threadIdx.x < 2) {
+    if (warp < 2) {  // warp w sums kind w and hands it to CTA `lane`
         double t = 0.0;
-        for (int w = 0; w < kPickWarps; ++w) t += sh.warp[threadIdx.x][w];
-        for (int r = 0; r < C; ++r)
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dsmem_map(smem_u32(&sh.cta[threadIdx.x][rank]), r)),
-                         "d"(t)
+        for (int w = 0; w < kPickWarps; ++w) t += sh.warp[warp][w];
+        if (lane < C)
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dsmem_map(smem_u32(&sh.cta[warp][rank]), lane)), "d"(t)
                          : "memory");
     }
     cluster_sync();
@@ -145,116 +227,158 @@ DEC_DEVINL double2 cluster_sum(PickShared& sh, double x, double y, int rank, int
     return t;
 }
 
-__global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs a) {
     __shared__ PickShared sh;
-    const int C = gridDim.x, rank = blockIdx.x, b = blockIdx.y;  // one cluster a sequence
+    const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;  // one cluster a sequence
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nb = drafts_of(a, b);
     const float T = a.temp ? a.temp[b] : 1.f;
     const bool warm = T > 0.f;
-    const double invT = warm ? 1.0 / (double)T : 0.0;
-    const float k = warm ? 1.4426950408889634f / T : 0.f;
+    const double c = warm ? 1.4426950408889634074 / (double)T : 0.0;  // e^(l / T) = 2^(c l)
+    const float k = log2e_over(T);
+    if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(threadIdx.x / 64.0);
+    pdl_wait();
 
-    // the whole row's max, sum and argmax from its pieces (each thread for itself)
-    auto row_stat = [&](int i) {
+    // ---- the rows' statistics from their pieces, a warp a row
+    for (int i = warp; i < 2 * a.n + 1; i += kPickWarps) {
+        const bool there = i > a.n ? a.draft && warm && i - a.n - 1 < nb : i <= nb;
+        if (!there) continue;
         const Stat* p = a.stats + ((size_t)b * (2 * a.n + 1) + i) * a.splits;
-        Stat z = p[0];
-        for (int s = 1; s < a.splits; ++s) {
-            const Stat y = p[s];
-            const float m = fmaxf(z.m, y.m);
-            z.s = m == -INFINITY ? 0.f : z.s * exp2f((z.m - m) * k) + y.s * exp2f((y.m - m) * k);
-            z.arg = z.m >= y.m ? z.arg : y.arg;
-            z.m = m;
+        Stat z{-INFINITY, 0.f, 0x7fffffff, 0};
+        for (int s = lane; s < a.splits; s += 32) z = join(z, p[s], k);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            Stat y;
+            y.m = __shfl_down_sync(0xffffffffu, z.m, o);
+            y.s = __shfl_down_sync(0xffffffffu, z.s, o);
+            y.arg = __shfl_down_sync(0xffffffffu, z.arg, o);
+            z = join(z, y, k);
         }
-        return z;
+        if (lane == 0) sh.row[i] = z;
+    }
+    __syncthreads();
+    auto target_row = [&](int i) { return a.target + b * a.t_seq + i * a.t_row; };
+    auto draft_row = [&](int i) { return a.draft ? a.draft + b * a.d_seq + i * a.d_row : nullptr; };
+    // e^((l - m) / T) in fp64
+    auto weight_of = [&](float l, float m) { return m > -INFINITY ? exp2_d(((double)l - (double)m) * c, sh.table) : 0.0; };
+
+    // ---- every draft's verdict by the fp32 sums, a thread a draft
+    if (threadIdx.x < nb) {
+        const int i = threadIdx.x, x = a.tok[(size_t)b * a.n + i];
+        const Stat p = sh.row[i];
+        int v = 0;
+        if (!warm) {
+            v = x == p.arg;
+        } else if (x >= 0 && x < a.V) {
+            // u q < p, multiplied out
+            const double u = a.u[(size_t)b * a.n + i];
+            double left = u * (double)p.s, right = weight_of(target_row(i)[x], p.m);
+            if (a.draft) {
+                const Stat q = sh.row[a.n + 1 + i];
+                left *= weight_of(draft_row(i)[x], q.m);
+                right *= (double)q.s;
+            }
+            v = left < right;
+            // the fp32 sums are within 1e-5 of the exact ones: a term is off by 2^-22 and by 2^-23 of its exponent,
+            // which is below 40 where the term counts
+            if (fabs(left - right) <= 4e-5 * fmax(left, right)) v = 2;
+        }
+        sh.verdict[i] = v;
+    }
+    __syncthreads();
+
+    // this thread's run of the vocabulary: E values, a multiple of 4
+    const int E = ((a.V + C * kPickThreads - 1) / (C * kPickThreads) + 3) & ~3;
+    const long long first = (long long)(rank * kPickThreads + (int)threadIdx.x) * E;
+    const int j0 = (int)min((long long)a.V, first), j1 = (int)min((long long)a.V, first + E);
+    // values j .. j + 3 of a row (-inf past the run's end)
+    auto load4 = [&](const float* row, int j) {
+        if (j + 4 <= j1 && ((uintptr_t)(row + j) & 15) == 0) return *reinterpret_cast<const float4*>(row + j);
+        float4 x;
+        x.x = j < j1 ? row[j] : -INFINITY;
+        x.y = j + 1 < j1 ? row[j + 1] : -INFINITY;
+        x.z = j + 2 < j1 ? row[j + 2] : -INFINITY;
+        x.w = j + 3 < j1 ? row[j + 3] : -INFINITY;
+        return x;
     };
-    const int per = (a.V + C * kPickWarps - 1) / (C * kPickWarps);  // a warp's run of the vocabulary
-    const int j0 = min(a.V, (rank * kPickWarps + warp) * per), j1 = min(a.V, j0 + per);
-    // fp64 sums of e^((l - m) / T) of the target row and of the draft row (null: 0)
+    // fp64 sums of a target row and of a draft row (null: 0)
     auto sums = [&](const float* pr, float pm, const float* qr, float qm) {
         double x = 0.0, y = 0.0;
-        for (int j = j0 + lane; j < j1; j += 32) {
-            if (pm > -INFINITY) x += exp(((double)pr[j] - (double)pm) * invT);
-            if (qr && qm > -INFINITY) y += exp(((double)qr[j] - (double)qm) * invT);
+        for (int j = j0; j < j1; j += 4) {
+            const float4 p = load4(pr, j);
+            x += (weight_of(p.x, pm) + weight_of(p.y, pm)) + (weight_of(p.z, pm) + weight_of(p.w, pm));
+            if (qr) {
+                const float4 q = load4(qr, j);
+                y += (weight_of(q.x, qm) + weight_of(q.y, qm)) + (weight_of(q.z, qm) + weight_of(q.w, qm));
+            }
         }
         return cluster_sum(sh, x, y, rank, C);
     };
 
     // ---- the first draft that is not accepted
-    int acc = 0, arg = 0;
+    int acc = 0;
+    double2 z = make_double2(0.0, 0.0);  // row acc's sums, where they are known
+    bool known = false;
     for (; acc < nb; ++acc) {
-        const int x = a.tok[(size_t)b * a.n + acc];
-        const Stat p = row_stat(acc);
-        if (!warm) {
-            if (x != p.arg) break;
-            continue;
+        int v = sh.verdict[acc];
+        if (v == 2) {
+            const int x = a.tok[(size_t)b * a.n + acc];
+            const float pm = sh.row[acc].m, qm = a.draft ? sh.row[a.n + 1 + acc].m : 0.f;
+            z = sums(target_row(acc), pm, draft_row(acc), qm);
+            const double q = a.draft ? weight_of(draft_row(acc)[x], qm) : 1.0;
+            v = (double)a.u[(size_t)b * a.n + acc] * q * z.x < weight_of(target_row(acc)[x], pm) * (a.draft ? z.y : 1.0);
+            known = !v;
         }
-        if (x < 0 || x >= a.V) break;
-        const float* pr = a.target + b * a.t_seq + acc * a.t_row;
-        const float* qr = a.draft ? a.draft + b * a.d_seq + acc * a.d_row : nullptr;
-        const double u = a.u[(size_t)b * a.n + acc];
-        const double ep = p.m > -INFINITY ? exp(((double)pr[x] - (double)p.m) * invT) : 0.0;
-        double left, right;
-        if (!qr) {
-            left = u * (double)p.s;
-            right = ep;
-        } else {
-            const Stat q = row_stat(a.n + 1 + acc);
-            const double eq = q.m > -INFINITY ? exp(((double)qr[x] - (double)q.m) * invT) : 0.0;
-            left = u * eq * (double)p.s;
-            right = ep * (double)q.s;
-        }
-        // the fp32 sums are within 1e-5 of the exact ones (each term within 2^-22 (l - m) / T,
-        // which is below 2^-22 * 40 where it counts)
-        if (fabs(left - right) <= 4e-5 * fmax(left, right)) {
-            const Stat q = qr ? row_stat(a.n + 1 + acc) : Stat{0.f, 1.f, 0, 0};
-            const double2 z = sums(pr, p.m, qr, q.m);
-            const double eq = !qr ? 1.0 : q.m > -INFINITY ? exp(((double)qr[x] - (double)q.m) * invT) : 0.0;
-            left = u * eq * z.x;
-            right = ep * (qr ? z.y : 1.0);
-        }
-        if (!(left < right)) break;
+        if (!v) break;
     }
-    const Stat p = row_stat(acc);
-    arg = p.arg;
-    int pick = -1;
-    if (!warm) {
-        pick = arg < a.V ? arg : -1;
-    } else if (p.m > -INFINITY) {
+    const Stat p = sh.row[acc];
+    int32_t* out = a.tokens + (size_t)b * (a.n + 1);
+    if (rank == 0) {
+        for (int i = threadIdx.x; i <= a.n; i += kPickThreads) {
+            if (i < acc) out[i] = a.tok[(size_t)b * a.n + i];
+            if (i == acc && !(warm && p.m > -INFINITY)) out[i] = !warm && p.arg < a.V ? p.arg : -1;
+            if (i > acc) out[i] = -1;
+        }
+        if (threadIdx.x == 0) a.accepted[b] = acc;
+    }
+    if (warm && p.m > -INFINITY) {
         // ---- draw from max(p - q, 0) of row acc, or from p after the last draft
-        const float* pr = a.target + b * a.t_seq + acc * a.t_row;
+        const float* pr = target_row(acc);
         const bool rej = acc < nb;
-        const float* qr = rej && a.draft ? a.draft + b * a.d_seq + acc * a.d_row : nullptr;
+        const float* qr = rej ? draft_row(acc) : nullptr;
         const int x = rej && !a.draft ? a.tok[(size_t)b * a.n + acc] : -1;
-        const float qm = qr ? row_stat(a.n + 1 + acc).m : -INFINITY;
-        const double2 z = sums(pr, p.m, qr, qm);
+        const float qm = qr ? sh.row[a.n + 1 + acc].m : -INFINITY;
+        if (!known) z = sums(pr, p.m, qr, qm);
         const double ip = 1.0 / z.x, iq = qr && z.y > 0.0 ? 1.0 / z.y : 0.0;
         bool plain = false;  // no weight left in p - q: p itself
-        auto weight = [&](int j) {
-            const double pj = exp(((double)pr[j] - (double)p.m) * invT) * ip;
+        auto weight = [&](float lp, float lq, int j) {
+            const double pj = weight_of(lp, p.m) * ip;
             if (plain) return pj;
             double qj = j == x ? 1.0 : 0.0;
-            if (iq > 0.0) qj = exp(((double)qr[j] - (double)qm) * invT) * iq;
+            if (qr) qj = weight_of(lq, qm) * iq;
             return fmax(pj - qj, 0.0);
         };
-        double own = 0.0;
-        double2 tot;
+        double own, total;
         for (;;) {
             own = 0.0;
-            for (int j = j0 + lane; j < j1; j += 32) own += weight(j);
-            tot = cluster_sum(sh, own, 0.0, rank, C);
-            if (tot.x > 0.0 || plain) break;
+            for (int j = j0; j < j1; j += 4) {
+                const float4 lp = load4(pr, j), lq = qr ? load4(qr, j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                own += (weight(lp.x, lq.x, j) + weight(lp.y, lq.y, j + 1)) +
+                       (weight(lp.z, lq.z, j + 2) + weight(lp.w, lq.w, j + 3));
+            }
+            total = cluster_sum(sh, own, 0.0, rank, C).x;
+            if (total > 0.0 || plain) break;
             plain = true;
         }
-        // the run of the vocabulary in which the cumulative weight passes us * total: the
-        // first one whose end is above it (the last one with any weight when rounding leaves none)
-        const double goal = (double)a.us[b] * tot.x;
-        double before = 0.0, upto = 0.0;
+        // The run in which the cumulative weight passes us * total: of CTAs, then of this CTA's warps, then of the
+        // warp's lanes, then of the lane's values, each time the first with weight whose end is above the goal (the
+        // last with weight, should rounding leave none).
+        const double goal = (double)a.us[b] * total;
+        double before = 0.0, base = 0.0;
         int cta = -1, w = -1;
-        double base = 0.0;
         for (int r = 0; r < C; ++r) {
-            upto = before + sh.cta[0][r];
-            if (sh.cta[0][r] > 0.0) {
+            const double s = sh.cta[0][r], upto = before + s;
+            if (s > 0.0) {
                 cta = r;
                 base = before;
                 if (upto > goal) break;
@@ -264,8 +388,8 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(VerifyArgs a)
         if (cta == rank) {
             before = base;
             for (int v = 0; v < kPickWarps; ++v) {
-                upto = before + sh.warp[0][v];
-                if (sh.warp[0][v] > 0.0) {
+                const double s = sh.warp[0][v], upto = before + s;
+                if (s > 0.0) {
                     w = v;
                     base = before;
                     if (upto > goal) break;
@@ -273,36 +397,47 @@ __global__ void __launch_bounds__(kPickThreads) verify_pick_kernel(VerifyArgs a)
                 before = upto;
             }
             if (w == warp) {
-                int last = -1;
-                double run = base;
-                for (int j = j0; j < j1 && pick < 0; j += 32) {
-                    const double wj = j + lane < j1 ? weight(j + lane) : 0.0;
-                    double c = wj;
+                double cum = own;
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const double y = __shfl_up_sync(0xffffffffu, c, o);
-                        if (lane >= o) c += y;
-                    }
-                    const unsigned some = __ballot_sync(0xffffffffu, wj > 0.0);
-                    const unsigned hit = __ballot_sync(0xffffffffu, wj > 0.0 && run + c > goal);
-                    if (hit) pick = j + __ffs(hit) - 1;
-                    if (some) last = j + 31 - __clz(some);
-                    run += __shfl_sync(0xffffffffu, c, 31);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double y = __shfl_up_sync(0xffffffffu, cum, o);
+                    if (lane >= o) cum += y;
                 }
-                if (pick < 0) pick = last;
-                if (lane == 0) a.tokens[(size_t)b * (a.n + 1) + acc] = pick;
+                const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
+                const unsigned hit = __ballot_sync(0xffffffffu, own > 0.0 && base + cum > goal);
+                const int who = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+                if (lane == who) {
+                    double run = base + (cum - own);
+                    int pick = -1;
+                    for (int j = j0; j < j1; ++j) {
+                        const double s = weight(pr[j], qr ? qr[j] : 0.f, j);
+                        if (s > 0.0) {
+                            pick = j;
+                            run += s;
+                            if (run > goal) break;
+                        }
+                    }
+                    out[acc] = pick;
+                }
             }
         }
     }
-    if (rank == 0) {
-        for (int i = threadIdx.x; i <= a.n; i += kPickThreads) {
-            if (i < acc) a.tokens[(size_t)b * (a.n + 1) + i] = a.tok[(size_t)b * a.n + i];
-            if (i > acc) a.tokens[(size_t)b * (a.n + 1) + i] = -1;
-            if (i == acc && (!warm || !(p.m > -INFINITY))) a.tokens[(size_t)b * (a.n + 1) + i] = pick;
-        }
-        if (threadIdx.x == 0) a.accepted[b] = acc;
-    }
     cluster_sync();  // no CTA leaves while another may still store to its shared memory
+}
+
+// Clusters of 16 CTAs need the kernel's consent, once a device.
+cudaError_t allow_wide_cluster() {
+    static std::mutex mu;
+    static std::set<int> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count(dev)) return cudaSuccess;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_pick_kernel),
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.insert(dev);
+    return e;
 }
 
 int verify_splits(int B, int n, int V) {
@@ -334,7 +469,7 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     if (!target || !u_sample || !n_accepted || !tokens || !workspace) return bad(DEC_ERR_INVALID_ARG, "NULL pointer");
     if (B <= 0 || n < 0 || V <= 0) return bad(DEC_ERR_INVALID_ARG, "bad B / n / V");
     if (n > 0 && (!draft_tok || !u_accept)) return bad(DEC_ERR_INVALID_ARG, "NULL pointer");
-    if (n > 64) return bad(DEC_ERR_UNSUPPORTED, "more than 64 drafted tokens");
+    if (n > kMaxDrafts) return bad(DEC_ERR_UNSUPPORTED, "more than 64 drafted tokens");
     if ((int64_t)B * (2 * n + 1) > 65535) return bad(DEC_ERR_UNSUPPORTED, "B * (2 n + 1) above 65535");
     if (V > (1 << 30)) return bad(DEC_ERR_UNSUPPORTED, "V above 2^30");
     if (target_row < V || target_seq < 0) return bad(DEC_ERR_INVALID_ARG, "bad target strides");
@@ -364,16 +499,23 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     verify_stats_kernel<<<dim3(a.splits, B * (2 * n + 1)), kStatThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = allow_wide_cluster();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kPickMaxCluster, B);
+    // as many CTAs a sequence as one wave of them allows: with few sequences the draw is shorter the more
+    // SMs it has, with many a second wave would cost what the wider cluster gains
+    int C = kPickCluster;
+    while (C > 1 && (int64_t)B * C > 148) C /= 2;
+    cfg.gridDim = dim3(C, B);
     cfg.blockDim = dim3(kPickThreads);
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kPickMaxCluster;
+    at[0].val.clusterDim.x = C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, verify_pick_kernel, a);
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("spec_verify: ") + cudaGetErrorString(e));
     return DEC_OK;
