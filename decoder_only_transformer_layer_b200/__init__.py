@@ -351,37 +351,67 @@ def weight_gemv_q8(Wq, scale, x, y, stream=None):
 
 # ---------------------------------------------------------------------- a step over a caller's paged cache
 
-def _want(name, t, dtype, shape, rows=False):
-    """Refuse a tensor of another type, shape, device kind or layout than the call takes: its
-    address alone goes to the library. ``rows``: the first dimensions may be strided, the
-    last is contiguous (two last ones for rows = 2)."""
+def _want(name, t, dtype, shape, rows=0):
+    """Refuse a tensor of another type, shape or layout than the call takes: its address alone goes
+    to the library. None in ``shape`` is any extent; with ``rows`` only that many last dimensions
+    have to be contiguous."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape))):
         raise ValueError(f"{name}: expected shape {tuple('*' if w is None else w for w in shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         step = 1
-        for n, st in zip(reversed(t.shape[t.dim() - int(rows):] if rows else t.shape),
-                         reversed(t.stride()[t.dim() - int(rows):] if rows else t.stride())):
+        for n, st in zip(reversed(t.shape[t.dim() - rows:] if rows else t.shape),
+                         reversed(t.stride()[t.dim() - rows:] if rows else t.stride())):
             if n > 1 and st != step:
                 raise ValueError(f"{name}: must be contiguous" + (" in its last dimensions" if rows else ""))
             step *= n
-    return t
 
 
-def _same_device(stream, *tensors):
-    """The tensors' one CUDA device, made current for the call, and the stream on it."""
-    import torch
-    dev = tensors[0].device
+def _fits(t, dtype, *shape):
+    """The checks of _want for a contiguous tensor, without the reasons."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _device(*tensors):
+    """The index of the tensors' one CUDA device."""
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("the tensors are on different devices")
-    if dev.type != "cuda":
+    if index < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    return torch.cuda.device(dev), (torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream))
+    return index
+
+
+def _launch(fn, index, stream, *args):
+    """Call an entry point with device `index` current, on `stream` or that device's current stream."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
+        _check(fn(*args, int(stream)))
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, int(stream)))
+
+
+def _step(t, dim):
+    """Stride of a dimension, for a single entry the extent of the ones below it."""
+    return t.stride(dim) if t.shape[dim] > 1 else t.shape[-1] * (t.shape[1] if dim == 0 else 1)
+
+
+def _workspace(workspace, need, index, stream):
+    import torch
+    if workspace is None:
+        if stream is not None and int(stream) != torch.cuda.current_stream(index).cuda_stream:
+            raise ValueError("a call on a stream that is not the current one needs its own workspace")
+        return torch.empty(need, dtype=torch.uint8, device=index)
+    _want("workspace", workspace, torch.uint8, (None,))
+    return workspace
 
 
 def paged_resize(old_len, new_len, block_table, free_pages, n_free, cu_rows, slot, row_pos, status, page_size=16,
@@ -390,24 +420,20 @@ def paged_resize(old_len, new_len, block_table, free_pages, n_free, cu_rows, slo
     Device int32 tensors: old_len, new_len [B]; block_table [B][max_pages]; free_pages [n_pages];
     n_free [1]; out: cu_rows [B + 1], slot and row_pos [T], status [1] (a STATUS code: nothing
     but the outputs changed unless it is 0)."""
-    import torch
-    i32 = torch.int32
+    from torch import int32 as i32
     _want("block_table", block_table, i32, (None, None))
     B, max_pages = block_table.shape
-    _want("old_len", old_len, i32, (B,))
-    _want("new_len", new_len, i32, (B,))
     _want("free_pages", free_pages, i32, (None,))
-    _want("n_free", n_free, i32, (1,))
-    _want("cu_rows", cu_rows, i32, (B + 1,))
     _want("slot", slot, i32, (None,))
     T = slot.shape[0]
-    _want("row_pos", row_pos, i32, (T,))
-    _want("status", status, i32, (1,))
-    guard, st = _same_device(stream, old_len, new_len, block_table, free_pages, n_free, cu_rows, slot, row_pos, status)
-    with guard:
-        _check(lib().paged_resize(old_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(), max_pages,
-                                  page_size, free_pages.data_ptr(), free_pages.shape[0], n_free.data_ptr(),
-                                  cu_rows.data_ptr(), slot.data_ptr(), row_pos.data_ptr(), T, status.data_ptr(), st))
+    for name, t, n in (("old_len", old_len, B), ("new_len", new_len, B), ("n_free", n_free, 1),
+                       ("cu_rows", cu_rows, B + 1), ("row_pos", row_pos, T), ("status", status, 1)):
+        if not _fits(t, i32, n):
+            _want(name, t, i32, (n,))
+    index = _device(old_len, new_len, block_table, free_pages, n_free, cu_rows, slot, row_pos, status)
+    _launch(lib().paged_resize, index, stream, old_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(),
+            max_pages, page_size, free_pages.data_ptr(), free_pages.shape[0], n_free.data_ptr(), cu_rows.data_ptr(),
+            slot.data_ptr(), row_pos.data_ptr(), T, status.data_ptr())
     return cu_rows, slot, row_pos
 
 
@@ -416,24 +442,26 @@ def paged_rope_append(qkv, slot, row_pos, q_out, k_pool, v_pool, rope_base, q_no
     """QK-norm, RoPE and cache append of QKV rows. Device tensors: qkv fp32 [T][(nq + 2 nkv) d]
     (rows may be strided); slot, row_pos int32 [T]; q_out bf16 [T][nq][d]; pools bf16
     [n_pages][nkv][page][d]; q_norm, k_norm fp32 [d] or None. Rows with a negative slot are skipped."""
-    import torch
-    _want("k_pool", k_pool, torch.bfloat16, (None, None, page_size, None))
+    from torch import bfloat16, float32, int32
+    _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
     n_pages, nkv, _, d = k_pool.shape
-    _want("v_pool", v_pool, torch.bfloat16, (n_pages, nkv, page_size, d))
-    _want("q_out", q_out, torch.bfloat16, (None, None, d))
+    if not _fits(v_pool, bfloat16, n_pages, nkv, page_size, d):
+        _want("v_pool", v_pool, bfloat16, (n_pages, nkv, page_size, d))
+    _want("q_out", q_out, bfloat16, (None, None, d))
     T, nq, _ = q_out.shape
-    _want("qkv", qkv, torch.float32, (T, (nq + 2 * nkv) * d), rows=1)
-    _want("slot", slot, torch.int32, (T,))
-    _want("row_pos", row_pos, torch.int32, (T,))
+    width = (nq + 2 * nkv) * d
+    if not _fits(qkv, float32, T, width):
+        _want("qkv", qkv, float32, (T, width), rows=1)
+    if not (_fits(slot, int32, T) and _fits(row_pos, int32, T)):
+        _want("slot", slot, int32, (T,))
+        _want("row_pos", row_pos, int32, (T,))
     for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
         if g is not None:
-            _want(name, g, torch.float32, (d,))
-    guard, st = _same_device(stream, qkv, slot, row_pos, q_out, k_pool, v_pool, q_norm, k_norm)
-    with guard:
-        _check(lib().paged_rope_append(qkv.data_ptr(), qkv.stride(0) if T > 1 else qkv.shape[1], _ptr(q_norm),
-                                       _ptr(k_norm), eps, rope_base, slot.data_ptr(), row_pos.data_ptr(), T, nq, nkv,
-                                       d, page_size, q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), n_pages,
-                                       st))
+            _want(name, g, float32, (d,))
+    index = _device(qkv, slot, row_pos, q_out, k_pool, v_pool, q_norm, k_norm)
+    _launch(lib().paged_rope_append, index, stream, qkv.data_ptr(), qkv.stride(0) if T > 1 else width, _ptr(q_norm),
+            _ptr(k_norm), eps, rope_base, slot.data_ptr(), row_pos.data_ptr(), T, nq, nkv, d, page_size,
+            q_out.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), n_pages)
     return q_out
 
 
@@ -444,24 +472,26 @@ def gqa_chunk_attn(q, k_pool, v_pool, block_table, cu_rows, kv_len, scale, out, 
     [B][max_pages]; cu_rows int32 [B + 1]; kv_len int32 [B] (new rows included); out bf16
     [T][nq][d]. workspace: a byte tensor of gqa_chunk_attn_workspace(d), or None for one
     allocated by torch for the call on the current stream (a call on another stream brings its own)."""
-    import torch
-    _want("k_pool", k_pool, torch.bfloat16, (None, None, page_size, None))
+    from torch import bfloat16, int32
+    _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
     n_pages, nkv, _, d = k_pool.shape
-    _want("v_pool", v_pool, torch.bfloat16, (n_pages, nkv, page_size, d))
-    _want("q", q, torch.bfloat16, (None, None, d), rows=2)
+    if not _fits(v_pool, bfloat16, n_pages, nkv, page_size, d):
+        _want("v_pool", v_pool, bfloat16, (n_pages, nkv, page_size, d))
+    _want("q", q, bfloat16, (None, None, d), rows=2)
     T, nq, _ = q.shape
-    _want("out", out, torch.bfloat16, (T, nq, d))
-    _want("block_table", block_table, torch.int32, (None, None))
+    if not _fits(out, bfloat16, T, nq, d):
+        _want("out", out, bfloat16, (T, nq, d))
+    _want("block_table", block_table, int32, (None, None))
     B, max_pages = block_table.shape
-    _want("cu_rows", cu_rows, torch.int32, (B + 1,))
-    _want("kv_len", kv_len, torch.int32, (B,))
-    guard, st = _same_device(stream, q, k_pool, v_pool, block_table, cu_rows, kv_len, out, workspace)
-    with guard:
-        workspace = _workspace(workspace, lib().gqa_chunk_attn_workspace(d), q.device, stream)
-        _check(lib().gqa_chunk_attn(q.data_ptr(), q.stride(0) if T > 1 else nq * d, k_pool.data_ptr(),
-                                    v_pool.data_ptr(), n_pages, block_table.data_ptr(), max_pages, cu_rows.data_ptr(),
-                                    kv_len.data_ptr(), B, T, nq, nkv, d, page_size, scale, window, softcap,
-                                    out.data_ptr(), workspace.data_ptr(), workspace.numel(), st))
+    if not (_fits(cu_rows, int32, B + 1) and _fits(kv_len, int32, B)):
+        _want("cu_rows", cu_rows, int32, (B + 1,))
+        _want("kv_len", kv_len, int32, (B,))
+    index = _device(q, k_pool, v_pool, block_table, cu_rows, kv_len, out, workspace)
+    L = lib()
+    workspace = _workspace(workspace, L.gqa_chunk_attn_workspace(d), index, stream)
+    _launch(L.gqa_chunk_attn, index, stream, q.data_ptr(), q.stride(0) if T > 1 else nq * d, k_pool.data_ptr(),
+            v_pool.data_ptr(), n_pages, block_table.data_ptr(), max_pages, cu_rows.data_ptr(), kv_len.data_ptr(), B, T,
+            nq, nkv, d, page_size, scale, window, softcap, out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -473,50 +503,31 @@ def spec_verify(target, draft, draft_tok, n_draft, temperature, u_accept, u_samp
     temperature fp32 [B] or None (1; <= 0 is greedy); u_accept fp32 [B][n] and u_sample fp32 [B] in
     [0, 1); out: n_accepted int32 [B], tokens int32 [B][n + 1] (accepted drafts, the next token,
     -1). workspace as in gqa_chunk_attn (spec_verify_workspace(B, n, V) bytes)."""
-    import torch
-    f32, i32 = torch.float32, torch.int32
-    _want("target", target, f32, (None, None, None), rows=1)
+    from torch import float32, int32
+    _want("target", target, float32, (None, None, None), rows=1)
     B, n1, V = target.shape
     n = n1 - 1
     if n < 0:
         raise ValueError("target: needs a row after the last draft")
     if draft is not None:
-        _want("draft", draft, f32, (B, n, V), rows=1)
-    _want("draft_tok", draft_tok, i32, (B, n))
+        _want("draft", draft, float32, (B, n, V), rows=1)
+    for name, t, dtype, shape in (("draft_tok", draft_tok, int32, (B, n)), ("u_accept", u_accept, float32, (B, n)),
+                                  ("u_sample", u_sample, float32, (B,)), ("n_accepted", n_accepted, int32, (B,)),
+                                  ("tokens", tokens, int32, (B, n1))):
+        if not _fits(t, dtype, *shape):
+            _want(name, t, dtype, shape)
     if n_draft is not None:
-        _want("n_draft", n_draft, i32, (B,))
+        _want("n_draft", n_draft, int32, (B,))
     if temperature is not None:
-        _want("temperature", temperature, f32, (B,))
-    _want("u_accept", u_accept, f32, (B, n))
-    _want("u_sample", u_sample, f32, (B,))
-    _want("n_accepted", n_accepted, i32, (B,))
-    _want("tokens", tokens, i32, (B, n1))
-    guard, st = _same_device(stream, target, draft, draft_tok, n_draft, temperature, u_accept, u_sample, n_accepted,
-                             tokens, workspace)
-    with guard:
-        workspace = _workspace(workspace, lib().spec_verify_workspace(B, n, V), target.device, stream)
-        _check(lib().spec_verify(target.data_ptr(), _step(target, 1), _step(target, 0), _ptr(draft),
-                                 0 if draft is None else _step(draft, 1), 0 if draft is None else _step(draft, 0),
-                                 draft_tok.data_ptr(), _ptr(n_draft), _ptr(temperature), u_accept.data_ptr(),
-                                 u_sample.data_ptr(), B, n, V, n_accepted.data_ptr(), tokens.data_ptr(),
-                                 workspace.data_ptr(), workspace.numel(), st))
+        _want("temperature", temperature, float32, (B,))
+    index = _device(target, draft, draft_tok, n_draft, temperature, u_accept, u_sample, n_accepted, tokens, workspace)
+    L = lib()
+    workspace = _workspace(workspace, L.spec_verify_workspace(B, n, V), index, stream)
+    _launch(L.spec_verify, index, stream, target.data_ptr(), _step(target, 1), _step(target, 0), _ptr(draft),
+            0 if draft is None else _step(draft, 1), 0 if draft is None else _step(draft, 0), draft_tok.data_ptr(),
+            _ptr(n_draft), _ptr(temperature), u_accept.data_ptr(), u_sample.data_ptr(), B, n, V, n_accepted.data_ptr(),
+            tokens.data_ptr(), workspace.data_ptr(), workspace.numel())
     return n_accepted, tokens
-
-
-def _step(t, dim):
-    """Stride of a dimension, for a single entry the extent of the ones below it."""
-    return t.stride(dim) if t.shape[dim] > 1 else t.shape[-1] * (t.shape[1] if dim == 0 else 1)
-
-
-def _workspace(workspace, need, device, stream):
-    import torch
-    if workspace is None:
-        if stream is not None and int(stream) != torch.cuda.current_stream(device).cuda_stream:
-            raise ValueError("a call on a stream that is not the current one needs its own workspace")
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous():
-        raise ValueError("workspace: expected a contiguous byte tensor")
-    return workspace
 
 
 def check_standalone(stream=None):

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <exception>
 #include <string>
 
@@ -32,14 +33,17 @@ dec_status bad(dec_status s, const std::string& why) {
 //   row t of sequence b  : position p = old_b + (t - cu_b), slot 16 page(p) + p % 16
 // both counted in the order (sequence, page). The given-back pages are stacked in
 // reverse, so resizing back restores the free list and the table exactly.
-// One cluster does it all: every CTA scans the lengths for itself (no exchange), the rows
-// and pages are spread over the cluster's threads, and cluster barriers separate checking
-// from writing, and reading the free list from stacking on it.
+// One cluster does the pages: every CTA scans the lengths for itself (no exchange), the
+// pages are spread over the cluster's threads, and cluster barriers separate checking
+// from writing, and reading the free list from stacking on it. A few thousand rows are
+// spread over it too; more rows have a kernel of their own on all SMs, which reads the
+// finished table (a 100,000-row step took 23 us with the rows in the cluster of 8 CTAs).
 // Latency is the bound: a few dependent memory round trips and the barriers.
 
 constexpr int kRzThreads = 1024;
 constexpr int kRzMaxB = 4096;  // prefix sums: 3 x 4097 int32 of shared memory
 constexpr int kRzPer = kRzMaxB / kRzThreads;
+constexpr int kRzRows = 4096;    // most rows that the cluster places itself
 
 struct ResizeArgs {
     const int32_t* old_len;
@@ -55,6 +59,7 @@ struct ResizeArgs {
     int32_t* row_pos;
     int T;
     int32_t* status;
+    bool rows_here;  // the rows are placed here, not by paged_slots_kernel
 };
 
 DEC_DEVINL int page_count(int len) { return len / kPage + (len % kPage != 0); }
@@ -82,6 +87,7 @@ __global__ void __launch_bounds__(kRzThreads) paged_resize_kernel(ResizeArgs a) 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank(), C = gridDim.x;  // the grid is one cluster
     const int gtid = rank * kRzThreads + tid, gn = C * kRzThreads;
+    if (!a.rows_here) pdl_trigger();
     if (tid == 0) flag = 0;
     // the matching wait comes before the first store to another CTA's flag
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -184,13 +190,13 @@ __global__ void __launch_bounds__(kRzThreads) paged_resize_kernel(ResizeArgs a) 
     if (flag) code = DEC_ERR_INVALID_ARG;
 
     if (code != DEC_OK) {
-        for (int i = gtid; i < a.T; i += gn) a.slot[i] = a.row_pos[i] = -1;
+        for (int i = gtid; a.rows_here && i < a.T; i += gn) a.slot[i] = a.row_pos[i] = -1;
         for (int b = gtid; b <= a.B; b += gn) a.cu_rows[b] = 0;
         if (gtid == 0) *a.status = code;
         return;
     }
     for (int b = gtid; b <= a.B; b += gn) a.cu_rows[b] = cu[b];
-    for (int i = gtid; i < a.T; i += gn) {
+    for (int i = gtid; a.rows_here && i < a.T; i += gn) {
         int slot = -1, p = -1;
         if (i < (int)n_rows) {
             const int b = find_seq(cu, a.B, i);
@@ -219,6 +225,23 @@ __global__ void __launch_bounds__(kRzThreads) paged_resize_kernel(ResizeArgs a) 
     }
 }
 
+// Slots and positions of the rows, from the table that paged_resize_kernel left (row starts of 0
+// after a failure: no rows).
+__global__ void __launch_bounds__(256) paged_slots_kernel(ResizeArgs a) {
+    pdl_wait();
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= a.T) return;
+    int slot = -1, p = -1;
+    if (i < a.cu_rows[a.B]) {
+        const int b = find_seq(a.cu_rows, a.B, i);
+        p = a.old_len[b] + (i - a.cu_rows[b]);
+        const int pg = a.table[(size_t)b * a.max_pages + p / kPage];
+        if (pg >= 0 && pg < a.n_pages) slot = pg * kPage + p % kPage;
+    }
+    a.slot[i] = slot;
+    a.row_pos[i] = p;
+}
+
 // ================================================================== paged_rope_append
 //
 // Row t of the fp32 QKV projection holds nq q heads, nkv k heads, nkv v heads of d values.
@@ -242,48 +265,84 @@ struct AppendArgs {
     uint16_t* k_pool;
     uint16_t* v_pool;
     int n_slots;
+    bool aligned;  // qkv's rows begin on 16 bytes
 };
 
+//
+// A block takes row after row (a grid of what the SMs hold at once); D / 8 lanes a head, each with
+// two runs of four values d / 2 apart, so every load is 16 bytes and every pair is in one lane. The
+// angles are fp64 in turns (p theta / 2 pi, reduced to [-1/2, 1/2]; theta by one pow a block), one
+// sine and cosine a pair and row, shared by all heads through shared memory.
+
+constexpr int kApThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_rope_append_kernel(AppendArgs a) {
-    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slot = a.slot[t], p = a.row_pos[t];
-    if (slot < 0 || slot >= a.n_slots) return;
-    constexpr int H = D / 2, N = H / 32;  // pairs a lane
-    float c[N], s[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) rope_cs(p, lane + 32 * k, D, a.base, &c[k], &s[k]);
-    const float* row = a.qkv + (size_t)t * a.ld;
-    const size_t page = slot / kPage, off = slot % kPage;
-    for (int h = warp; h < a.nq + 2 * a.nkv; h += 4) {
-        const bool isq = h < a.nq, isv = h >= a.nq + a.nkv;
-        float x[N], y[N];
-        float ss = 0.f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            x[k] = row[(size_t)h * D + lane + 32 * k];
-            y[k] = row[(size_t)h * D + H + lane + 32 * k];
-            ss += x[k] * x[k] + y[k] * y[k];
-        }
-        const float* g = isq ? a.q_norm : a.k_norm;
-        uint16_t* dst;
-        if (isq) {
-            dst = a.q_out + ((size_t)t * a.nq + h) * D;
-        } else {
-            const int j = isv ? h - a.nq - a.nkv : h - a.nq;
-            dst = (isv ? a.v_pool : a.k_pool) + ((page * a.nkv + j) * kPage + off) * D;
-        }
-        const bool norm = !isv && g != nullptr;
-        const float r = norm ? 1.0f / sqrtf(warp_sum(ss) / D + a.eps) : 1.f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int i = lane + 32 * k;
-            if (norm) {
-                x[k] = x[k] * r * g[i];
-                y[k] = y[k] * r * g[i + H];
+__global__ void __launch_bounds__(kApThreads, 4) paged_rope_append_kernel(AppendArgs a) {
+    constexpr int H = D / 2, LH = D / 8;     // lanes of a head
+    constexpr int kAtOnce = kApThreads / LH;  // heads a block has in hand
+    __shared__ float2 cs[2][H];               // (cos, sin) of the row, double-buffered
+    const int tid = threadIdx.x, sub = tid % LH, head0 = tid / LH;
+    double turns = 0.0;  // theta_i / 2 pi
+    if (tid < H) turns = pow((double)a.base, -2.0 * tid / D) * 0.15915494309189533577;
+    const int heads = a.nq + 2 * a.nkv;
+    float4 gq0, gq1, gk0, gk1;
+    if (a.q_norm) gq0 = *reinterpret_cast<const float4*>(a.q_norm + 4 * sub), gq1 = *reinterpret_cast<const float4*>(a.q_norm + H + 4 * sub);
+    if (a.k_norm) gk0 = *reinterpret_cast<const float4*>(a.k_norm + 4 * sub), gk1 = *reinterpret_cast<const float4*>(a.k_norm + H + 4 * sub);
+    int buf = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int slot = a.slot[t], p = a.row_pos[t];
+        if (slot < 0 || slot >= a.n_slots) continue;  // the whole block
+        const float* row = a.qkv + (size_t)t * a.ld;
+        // the first heads' values are on their way while the angles are worked out
+        float4 x, y;
+        auto load = [&](int h) {
+            const float* src = row + (size_t)h * D + 4 * sub;
+            if (a.aligned) {
+                x = __ldcs(reinterpret_cast<const float4*>(src));
+                y = __ldcs(reinterpret_cast<const float4*>(src + H));
+            } else {
+                x = make_float4(src[0], src[1], src[2], src[3]);
+                y = make_float4(src[H], src[H + 1], src[H + 2], src[H + 3]);
             }
-            dst[i] = f2bf(isv ? x[k] : x[k] * c[k] - y[k] * s[k]);
-            dst[i + H] = f2bf(isv ? y[k] : y[k] * c[k] + x[k] * s[k]);
+        };
+        if (head0 < heads) load(head0);
+        if (tid < H) {
+            const double r = (double)p * turns, f = r - rint(r);
+            float c, s;
+            sincospif((float)(2.0 * f), &s, &c);
+            cs[buf][tid] = make_float2(c, s);
+        }
+        __syncthreads();
+        const float4 cs01 = *reinterpret_cast<const float4*>(&cs[buf][4 * sub]);
+        const float4 cs23 = *reinterpret_cast<const float4*>(&cs[buf][4 * sub + 2]);
+        buf ^= 1;
+        const size_t page = slot / kPage, off = slot % kPage;
+        for (int h = head0; h < heads; h += kAtOnce) {
+            float4 u = x, v = y;
+            if (h + kAtOnce < heads) load(h + kAtOnce);
+            const bool isq = h < a.nq, isv = h >= a.nq + a.nkv;
+            const int j = isq ? h : isv ? h - a.nq - a.nkv : h - a.nq;
+            uint16_t* dst = isq ? a.q_out + ((size_t)t * a.nq + j) * D
+                                : (isv ? a.v_pool : a.k_pool) + ((page * a.nkv + j) * kPage + off) * D;
+            if (!isv) {
+                if (isq ? a.q_norm != nullptr : a.k_norm != nullptr) {
+                    float ss = u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w + v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+                    const unsigned group = (LH == 32 ? 0xffffffffu : ((1u << LH) - 1)) << (tid & 31 & ~(LH - 1));
+#pragma unroll
+                    for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+                    const float r = 1.0f / sqrtf(ss / D + a.eps);
+                    const float4 g0 = isq ? gq0 : gk0, g1 = isq ? gq1 : gk1;
+                    u.x = u.x * r * g0.x, u.y = u.y * r * g0.y, u.z = u.z * r * g0.z, u.w = u.w * r * g0.w;
+                    v.x = v.x * r * g1.x, v.y = v.y * r * g1.y, v.z = v.z * r * g1.z, v.w = v.w * r * g1.w;
+                }
+                const float4 s = u, w = v;
+                u.x = s.x * cs01.x - w.x * cs01.y, v.x = w.x * cs01.x + s.x * cs01.y;
+                u.y = s.y * cs01.z - w.y * cs01.w, v.y = w.y * cs01.z + s.y * cs01.w;
+                u.z = s.z * cs23.x - w.z * cs23.y, v.z = w.z * cs23.x + s.z * cs23.y;
+                u.w = s.w * cs23.z - w.w * cs23.w, v.w = w.w * cs23.z + s.w * cs23.w;
+            }
+            *reinterpret_cast<uint2*>(dst + 4 * sub) = make_uint2(pack_bf2(u.x, u.y), pack_bf2(u.z, u.w));
+            *reinterpret_cast<uint2*>(dst + H + 4 * sub) = make_uint2(pack_bf2(v.x, v.y), pack_bf2(v.z, v.w));
         }
     }
 }
@@ -309,9 +368,9 @@ dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t 
     if (n_pages > INT32_MAX / kPage || max_pages > INT32_MAX / kPage)
         return bad(DEC_ERR_UNSUPPORTED, "slots and positions must fit 32 bits");
     ResizeArgs a{old_len, new_len, B, block_table, max_pages, free_pages, n_pages, n_free, cu_rows, slot, row_pos, T,
-                 status};
-    int C = 1;
-    while (C < 8 && T > C * 4 * kRzThreads) C *= 2;
+                 status, T <= kRzRows};
+    // one CTA for a decode step; eight where many pages may move (a step of many rows or sequences)
+    const int C = T > kRzRows || B > 256 ? 8 : 1;
     const int smem = 3 * (B + 1) * (int)sizeof(int32_t);
     cudaError_t e = ensure_smem(reinterpret_cast<const void*>(paged_resize_kernel), smem);
     cudaLaunchConfig_t cfg = {};
@@ -326,6 +385,14 @@ dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t 
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, paged_resize_kernel, a);
+    if (e == cudaSuccess && !a.rows_here) {
+        cfg.gridDim = dim3((T + 255) / 256);
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        e = cudaLaunchKernelEx(&cfg, paged_slots_kernel, a);
+    }
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("paged_resize: ") + cudaGetErrorString(e));
     return DEC_OK;
 } catch (const std::exception&) {
@@ -347,14 +414,18 @@ dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, 
     const int64_t width = ((int64_t)nq + 2 * (int64_t)nkv) * d;
     if (ld < width) return bad(DEC_ERR_INVALID_ARG, "ld is smaller than a row");
     if (n_pages > INT32_MAX / kPage) return bad(DEC_ERR_UNSUPPORTED, "slots must fit 32 bits");
+    if (((uintptr_t)q_out | (uintptr_t)k_pool | (uintptr_t)v_pool | (uintptr_t)q_norm | (uintptr_t)k_norm) % 16 != 0)
+        return bad(DEC_ERR_UNSUPPORTED, "q_out, the pools and the norm gains must be 16-byte aligned");
     if (T == 0) return DEC_OK;
     AppendArgs a{qkv, ld, q_norm, k_norm, eps, rope_base, slot, row_pos, T, nq, nkv, static_cast<uint16_t*>(q_out),
-                 static_cast<uint16_t*>(k_pool), static_cast<uint16_t*>(v_pool), n_pages * kPage};
+                 static_cast<uint16_t*>(k_pool), static_cast<uint16_t*>(v_pool), n_pages * kPage,
+                 ((uintptr_t)qkv | (uintptr_t)(ld * 4)) % 16 == 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int grid = std::min(T, 148 * 4);
     if (d == 128)
-        paged_rope_append_kernel<128><<<T, 128, 0, st>>>(a);
+        paged_rope_append_kernel<128><<<grid, kApThreads, 0, st>>>(a);
     else
-        paged_rope_append_kernel<64><<<T, 128, 0, st>>>(a);
+        paged_rope_append_kernel<64><<<grid, kApThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("paged_rope_append: ") + cudaGetErrorString(e));
     return DEC_OK;

@@ -170,20 +170,48 @@ constexpr int kPickCluster = 16;  // most CTAs of a sequence
 // table, the exponential series of f ln 2 up to the 5th power (the next term is below 2^-54), n into
 // the exponent. Below 2^-1000 it is 0, which no sum of at most 2^30 terms with a term of 1 among
 // them can tell. 10 fp64 operations; the series alone took 18, and fp64 is what bounds the draw.
-DEC_DEVINL double exp2_d(double x, const double* table) {
+// N values side by side, so that each step's latency is shared.
+template <int N>
+DEC_DEVINL void exp2_d(double (&x)[N], const double* table) {
     constexpr double kLn2 = 0.69314718055994530942, kMagic = 105553116266496.0;  // 1.5 x 2^46: steps of 1/64
-    const double t = x + kMagic;
-    const double f = x - (t - kMagic);
-    double p = kLn2 * kLn2 * kLn2 * kLn2 * kLn2 / 120.0;
-    p = fma(p, f, kLn2 * kLn2 * kLn2 * kLn2 / 24.0);
-    p = fma(p, f, kLn2 * kLn2 * kLn2 / 6.0);
-    p = fma(p, f, kLn2 * kLn2 / 2.0);
-    p = fma(p, f, kLn2);
-    p = fma(p, f, 1.0);
-    const int n = __double2loint(t);
-    p *= table[n & 63];
-    return x > -1000.0 ? __hiloint2double(__double2hiint(p) + ((n >> 6) << 20), __double2loint(p)) : 0.0;
+    constexpr double c5 = kLn2 * kLn2 * kLn2 * kLn2 * kLn2 / 120.0, c4 = kLn2 * kLn2 * kLn2 * kLn2 / 24.0,
+                     c3 = kLn2 * kLn2 * kLn2 / 6.0, c2 = kLn2 * kLn2 / 2.0;
+    double f[N], p[N], w[N];
+    int n[N];
+    bool in[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        // -1000 and above, by the upper word (0xC08F4000 is -1000's); NaN counts as below
+        in[i] = (unsigned)__double2hiint(x[i]) < 0xC08F4000u;
+        const double t = x[i] + kMagic;
+        n[i] = __double2loint(t);
+        f[i] = x[i] - (t - kMagic);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = table[n[i] & 63];
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma(c5, f[i], c4);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma(p[i], f[i], c3);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma(p[i], f[i], c2);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma(p[i], f[i], kLn2);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = fma(p[i], f[i], 1.0) * w[i];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        x[i] = in[i] ? __hiloint2double(__double2hiint(p[i]) + ((n[i] >> 6) << 20), __double2loint(p[i])) : 0.0;
 }
+
+// Values of the vocabulary a lane has, with C CTAs a sequence.
+__host__ __device__ inline int run_per_lane(int V, int C) {
+    const long long lanes = (long long)C * kPickThreads;
+    return (int)(((V + lanes - 1) / lanes + 3) / 4 * 4);
+}
+
+// Values a thread keeps between the two passes of the draw, where that is all it has (KEEP).
+constexpr int kKeep = 16;
 
 struct PickShared {
     Stat row[2 * kMaxDrafts + 1];
@@ -227,7 +255,8 @@ DEC_DEVINL double2 cluster_sum(PickShared& sh, double x, double y, int rank, int
     return t;
 }
 
-__global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs a) {
+template <bool KEEP>
+__global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs a) {
     __shared__ PickShared sh;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;  // one cluster a sequence
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -259,8 +288,18 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
     __syncthreads();
     auto target_row = [&](int i) { return a.target + b * a.t_seq + i * a.t_row; };
     auto draft_row = [&](int i) { return a.draft ? a.draft + b * a.d_seq + i * a.d_row : nullptr; };
-    // e^((l - m) / T) in fp64
-    auto weight_of = [&](float l, float m) { return m > -INFINITY ? exp2_d(((double)l - (double)m) * c, sh.table) : 0.0; };
+    // e^((l - m) / T) in fp64; a row of -inf counts from 0, and every weight is 0
+    auto origin = [](float m) { return m > -INFINITY ? (double)m : 0.0; };
+    auto weight_of = [&](float l, double m) {
+        double x[1] = {((double)l - m) * c};
+        exp2_d(x, sh.table);
+        return x[0];
+    };
+    auto weights_of = [&](const float (&l)[4], double m, double (&x)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ((double)l[i] - m) * c;
+        exp2_d(x, sh.table);
+    };
 
     // ---- every draft's verdict by the fp32 sums, a thread a draft
     if (threadIdx.x < nb) {
@@ -272,10 +311,10 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
         } else if (x >= 0 && x < a.V) {
             // u q < p, multiplied out
             const double u = a.u[(size_t)b * a.n + i];
-            double left = u * (double)p.s, right = weight_of(target_row(i)[x], p.m);
+            double left = u * (double)p.s, right = weight_of(target_row(i)[x], origin(p.m));
             if (a.draft) {
                 const Stat q = sh.row[a.n + 1 + i];
-                left *= weight_of(draft_row(i)[x], q.m);
+                left *= weight_of(draft_row(i)[x], origin(q.m));
                 right *= (double)q.s;
             }
             v = left < right;
@@ -287,32 +326,59 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
     }
     __syncthreads();
 
-    // this thread's run of the vocabulary: E values, a multiple of 4
-    const int E = ((a.V + C * kPickThreads - 1) / (C * kPickThreads) + 3) & ~3;
-    const long long first = (long long)(rank * kPickThreads + (int)threadIdx.x) * E;
-    const int j0 = (int)min((long long)a.V, first), j1 = (int)min((long long)a.V, first + E);
-    // values j .. j + 3 of a row (-inf past the run's end)
-    auto load4 = [&](const float* row, int j) {
-        if (j + 4 <= j1 && ((uintptr_t)(row + j) & 15) == 0) return *reinterpret_cast<const float4*>(row + j);
-        float4 x;
-        x.x = j < j1 ? row[j] : -INFINITY;
-        x.y = j + 1 < j1 ? row[j + 1] : -INFINITY;
-        x.z = j + 2 < j1 ? row[j + 2] : -INFINITY;
-        x.w = j + 3 < j1 ? row[j + 3] : -INFINITY;
-        return x;
-    };
-    // fp64 sums of a target row and of a draft row (null: 0)
-    auto sums = [&](const float* pr, float pm, const float* qr, float qm) {
-        double x = 0.0, y = 0.0;
-        for (int j = j0; j < j1; j += 4) {
-            const float4 p = load4(pr, j);
-            x += (weight_of(p.x, pm) + weight_of(p.y, pm)) + (weight_of(p.z, pm) + weight_of(p.w, pm));
-            if (qr) {
-                const float4 q = load4(qr, j);
-                y += (weight_of(q.x, qm) + weight_of(q.y, qm)) + (weight_of(q.z, qm) + weight_of(q.w, qm));
-            }
+    // The vocabulary in runs of 32 E values, one a warp (E a multiple of 4): in step t of E / 4 lane l takes
+    // values 128 t + 4 l .. + 3 of the run, so that a warp reads whole lines.
+    const int E = run_per_lane(a.V, C);
+    const long long run0 = (long long)(rank * kPickWarps + warp) * 32 * E;
+    // values j .. j + 3 of a row (-inf past the vocabulary's end)
+    auto load4 = [&](const float* row, long long j, float (&x)[4]) {
+        if (j + 4 <= a.V && ((uintptr_t)(row + j) & 15) == 0) {
+            const float4 v = *reinterpret_cast<const float4*>(row + j);
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = j + q < a.V ? row[j + q] : -INFINITY;
         }
-        return cluster_sum(sh, x, y, rank, C);
+    };
+    double keep_p[kKeep], keep_q[kKeep];  // (KEEP)
+    // fp64 sums of a target row and of a draft row (null: 0)
+    auto sums = [&](const float* pr, double pm, const float* qr, double qm) {
+        double x[2] = {0.0, 0.0}, y[2] = {0.0, 0.0};
+        auto step = [&](int t) {
+            float p[4], q[4];
+            load4(pr, run0 + 128 * t + 4 * lane, p);
+            if (qr) load4(qr, run0 + 128 * t + 4 * lane, q);
+            double e[4];
+            weights_of(p, pm, e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (KEEP) keep_p[(4 * t + i) % kKeep] = e[i];
+                x[i & 1] += e[i];
+            }
+            if (qr) {
+                weights_of(q, qm, e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (KEEP) keep_q[(4 * t + i) % kKeep] = e[i];
+                    y[i & 1] += e[i];
+                }
+            }
+        };
+        if (KEEP) {
+#pragma unroll
+            for (int t = 0; t < kKeep / 4; ++t) {
+                if (4 * t < E) {
+                    step(t);
+                } else {  // past the run
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) keep_p[4 * t + i] = keep_q[4 * t + i] = 0.0;
+                }
+            }
+        } else {
+#pragma unroll 2
+            for (int t = 0; t < E / 4; ++t) step(t);
+        }
+        return cluster_sum(sh, x[0] + x[1], y[0] + y[1], rank, C);
     };
 
     // ---- the first draft that is not accepted
@@ -323,7 +389,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
         int v = sh.verdict[acc];
         if (v == 2) {
             const int x = a.tok[(size_t)b * a.n + acc];
-            const float pm = sh.row[acc].m, qm = a.draft ? sh.row[a.n + 1 + acc].m : 0.f;
+            const double pm = origin(sh.row[acc].m), qm = a.draft ? origin(sh.row[a.n + 1 + acc].m) : 0.0;
             z = sums(target_row(acc), pm, draft_row(acc), qm);
             const double q = a.draft ? weight_of(draft_row(acc)[x], qm) : 1.0;
             v = (double)a.u[(size_t)b * a.n + acc] * q * z.x < weight_of(target_row(acc)[x], pm) * (a.draft ? z.y : 1.0);
@@ -346,73 +412,92 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
         const float* pr = target_row(acc);
         const bool rej = acc < nb;
         const float* qr = rej ? draft_row(acc) : nullptr;
-        const int x = rej && !a.draft ? a.tok[(size_t)b * a.n + acc] : -1;
-        const float qm = qr ? sh.row[a.n + 1 + acc].m : -INFINITY;
-        if (!known) z = sums(pr, p.m, qr, qm);
-        const double ip = 1.0 / z.x, iq = qr && z.y > 0.0 ? 1.0 / z.y : 0.0;
+        // a point mass at a token outside the vocabulary takes nothing away
+        const int tok = rej && !a.draft ? a.tok[(size_t)b * a.n + acc] : -1, x = tok < a.V ? tok : -1;
+        const double pm = origin(p.m), qm = qr ? origin(sh.row[a.n + 1 + acc].m) : 0.0;
+        if (!known) z = sums(pr, pm, qr, qm);
+        // drawing from p alone, the sums just taken are the weights' (times 1 / z.x): no second pass
+        const bool bare = !qr && x < 0;
+        const double ip = bare ? 1.0 : 1.0 / z.x, iq = qr && z.y > 0.0 ? 1.0 / z.y : 0.0;
         bool plain = false;  // no weight left in p - q: p itself
-        auto weight = [&](float lp, float lq, int j) {
-            const double pj = weight_of(lp, p.m) * ip;
-            if (plain) return pj;
-            double qj = j == x ? 1.0 : 0.0;
-            if (qr) qj = weight_of(lq, qm) * iq;
-            return fmax(pj - qj, 0.0);
+        auto weight = [&](double ep, double eq, long long j) {
+            double w = ep * ip;
+            if (plain) return w;
+            if (qr) w -= eq * iq;
+            if (j == x) w -= 1.0;
+            return fmax(w, 0.0);
         };
-        double own, total;
-        for (;;) {
-            own = 0.0;
-            for (int j = j0; j < j1; j += 4) {
-                const float4 lp = load4(pr, j), lq = qr ? load4(qr, j) : make_float4(0.f, 0.f, 0.f, 0.f);
-                own += (weight(lp.x, lq.x, j) + weight(lp.y, lq.y, j + 1)) +
-                       (weight(lp.z, lq.z, j + 2) + weight(lp.w, lq.w, j + 3));
+        double total = z.x;
+        while (!bare) {
+            double own[2] = {0.0, 0.0};
+            if (KEEP) {
+#pragma unroll
+                for (int i = 0; i < kKeep; ++i)
+                    own[i & 1] += weight(keep_p[i], qr ? keep_q[i] : 0.0, run0 + 128 * (i / 4) + 4 * lane + i % 4);
+            } else {
+#pragma unroll 2
+                for (int t = 0; t < E / 4; ++t) {
+                    const long long j = run0 + 128 * t + 4 * lane;
+                    float lp[4], lq[4];
+                    load4(pr, j, lp);
+                    if (qr) load4(qr, j, lq);
+                    double ep[4], eq[4] = {0.0, 0.0, 0.0, 0.0};
+                    weights_of(lp, pm, ep);
+                    if (qr) weights_of(lq, qm, eq);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) own[i & 1] += weight(ep[i], eq[i], j + i);
+                }
             }
-            total = cluster_sum(sh, own, 0.0, rank, C).x;
+            total = cluster_sum(sh, own[0] + own[1], 0.0, rank, C).x;
             if (total > 0.0 || plain) break;
             plain = true;
         }
-        // The run in which the cumulative weight passes us * total: of CTAs, then of this CTA's warps, then of the
-        // warp's lanes, then of the lane's values, each time the first with weight whose end is above the goal (the
-        // last with weight, should rounding leave none).
+        // The place where the cumulative weight passes us * total: the CTA, its warp's run, then (all warps of the CTA
+        // sharing that run, 2 E values a warp) the warp, the lane and the value, each time the first with weight
+        // whose end is above the goal (the last with weight, should rounding leave none).
         const double goal = (double)a.us[b] * total;
-        double before = 0.0, base = 0.0;
-        int cta = -1, w = -1;
-        for (int r = 0; r < C; ++r) {
-            const double s = sh.cta[0][r], upto = before + s;
-            if (s > 0.0) {
-                cta = r;
-                base = before;
-                if (upto > goal) break;
-            }
-            before = upto;
-        }
-        if (cta == rank) {
-            before = base;
-            for (int v = 0; v < kPickWarps; ++v) {
-                const double s = sh.warp[0][v], upto = before + s;
-                if (s > 0.0) {
-                    w = v;
-                    base = before;
+        auto find = [&](const double* s, int n, double* base) {
+            double before = *base;
+            int at = -1;
+            for (int r = 0; r < n; ++r) {
+                const double upto = before + s[r];
+                if (s[r] > 0.0) {
+                    at = r;
+                    *base = before;
                     if (upto > goal) break;
                 }
                 before = upto;
             }
-            if (w == warp) {
-                double cum = own;
+            return at;
+        };
+        double base = 0.0;
+        if (find(sh.cta[0], C, &base) == rank) {
+            const int w = find(sh.warp[0], kPickWarps, &base);
+            const int per = E / 16 > 0 ? (E + 15) / 16 : 1;  // values a lane has of the run: 512 lanes, 32 E values
+            const long long begin = (long long)(rank * kPickWarps + w) * 32 * E, end = min((long long)a.V, begin + 32 * E);
+            const long long j = begin + (long long)threadIdx.x * per;
+            double own = 0.0;
+            for (int i = 0; i < per; ++i)
+                if (j + i < end) own += weight(weight_of(pr[j + i], pm), qr ? weight_of(qr[j + i], qm) : 0.0, j + i);
+            double cum = own;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, cum, o);
-                    if (lane >= o) cum += y;
-                }
+            for (int o = 1; o < 32; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, cum, o);
+                if (lane >= o) cum += y;
+            }
+            __syncthreads();  // sh.warp has been read
+            if (lane == 31) sh.warp[0][warp] = cum;
+            __syncthreads();
+            if (find(sh.warp[0], kPickWarps, &base) == warp) {
                 const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
                 const unsigned hit = __ballot_sync(0xffffffffu, own > 0.0 && base + cum > goal);
-                const int who = hit ? __ffs(hit) - 1 : 31 - __clz(some);
-                if (lane == who) {
+                if (lane == (hit ? __ffs(hit) - 1 : 31 - __clz(some))) {
                     double run = base + (cum - own);
                     int pick = -1;
-                    for (int j = j0; j < j1; ++j) {
-                        const double s = weight(pr[j], qr ? qr[j] : 0.f, j);
+                    for (int i = 0; i < per && j + i < end; ++i) {
+                        const double s = weight(weight_of(pr[j + i], pm), qr ? weight_of(qr[j + i], qm) : 0.0, j + i);
                         if (s > 0.0) {
-                            pick = j;
+                            pick = (int)(j + i);
                             run += s;
                             if (run > goal) break;
                         }
@@ -434,8 +519,11 @@ cudaError_t allow_wide_cluster() {
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     if (done.count(dev)) return cudaSuccess;
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_pick_kernel),
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_pick_kernel<true>),
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_pick_kernel<false>),
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) done.insert(dev);
     return e;
 }
@@ -516,7 +604,8 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, verify_pick_kernel, a);
+    if (e == cudaSuccess)
+        e = cudaLaunchKernelEx(&cfg, run_per_lane(V, C) <= kKeep ? verify_pick_kernel<true> : verify_pick_kernel<false>, a);
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("spec_verify: ") + cudaGetErrorString(e));
     return DEC_OK;
 } catch (const std::exception&) {

@@ -376,7 +376,8 @@ dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t 
  *           p * rope_base^(-2i/d), evaluated in fp64)
  *   q_out   device bf16 [T][nq][d]; k_pool/v_pool device bf16 [n_pages][nkv][16][d]
  * d must be 64 or 128, page_size 16. Errors: NULL pointer, a bad size or ld below
- * (nq + 2 nkv) d -> INVALID_ARG; else UNSUPPORTED. T = 0 does nothing. */
+ * (nq + 2 nkv) d -> INVALID_ARG; another d or page_size, or q_out, a pool or a gain off the
+ * 16-byte grid (qkv may lie anywhere) -> UNSUPPORTED. T = 0 does nothing. */
 dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, const float* k_norm, float eps,
                              float rope_base, const int32_t* slot, const int32_t* row_pos, int32_t T, int32_t nq,
                              int32_t nkv, int32_t d, int32_t page_size, void* q_out, void* k_pool, void* v_pool,

@@ -37,7 +37,9 @@ CASES += [("paged_rope_append", APPEND, BAD, {k: None}) for k in
 CASES += [("paged_rope_append", APPEND, s, c) for s, c in (
     (BAD, dict(T=-1)), (BAD, dict(nq=0)), (BAD, dict(nkv=0)), (BAD, dict(ld=1535)), (BAD, dict(rope_base=0.0)),
     (BAD, dict(rope_base=nan())), (BAD, dict(q_norm=P, eps=nan())), (BAD, dict(k_norm=P, eps=-1.0)),
-    (UNSUP, dict(d=96)), (UNSUP, dict(page_size=8)), (UNSUP, dict(n_pages=1 << 28)), (BAD, dict(n_pages=0)))]
+    (UNSUP, dict(d=96)), (UNSUP, dict(page_size=8)), (UNSUP, dict(n_pages=1 << 28)), (BAD, dict(n_pages=0)),
+    (UNSUP, dict(q_out=P + 8)), (UNSUP, dict(k_pool=P + 2)), (UNSUP, dict(v_pool=P + 4)), (UNSUP, dict(q_norm=P + 4)),
+    (UNSUP, dict(k_norm=P + 8)))]
 CASES += [("gqa_chunk_attn", CHUNK, BAD, {k: None}) for k in
           ("q", "k_pool", "v_pool", "block_table", "cu_rows", "kv_len", "out", "workspace")]
 CASES += [("gqa_chunk_attn", CHUNK, s, c) for s, c in (
