@@ -174,7 +174,7 @@ DEC_HD int lo_key(const ChunkArgs& a, const Seq& s, int t0) {
 
 // What a tile costs beside its blocks (filling the pipeline, the epilogue), in blocks: the runs are
 // equal in tiles' costs. A tile's units are kTileCost for nothing, then one for each block.
-constexpr int kTileCost = 3;
+constexpr int kTileCost = 4;
 // The block at which unit u of a tile lies; a run that ends within the first units has none of it.
 DEC_HD int block_at(int u) { return u > kTileCost ? u - kTileCost : 0; }
 
@@ -197,10 +197,17 @@ DEC_HD int tile_blocks(const ChunkArgs& a, const Seq& s, int t) {
     return hi_key(s, t1) / kKeys - lo_key(a, s, t0) / kKeys + 1;
 }
 
+constexpr int kFewTiles = 32;  // so many are summed one by one, which is shorter than the closed form
+
 // Units of one kv head of a sequence.
 DEC_HD long long seq_units(const ChunkArgs& a, const Seq& s) {
     if (s.n == 0) return 0;
     const int nt = tile_count(a, s);
+    if (nt <= kFewTiles) {
+        int u = 0;
+        for (int t = 0; t < nt; ++t) u += kTileCost + tile_blocks(a, s, t);
+        return u;
+    }
     return units_before(a, s, nt - 1) + kTileCost + tile_blocks(a, s, nt - 1);
 }
 
@@ -240,15 +247,20 @@ DEC_HD Run run_from(const ChunkArgs& a, int b, long long before, const Cut& cut,
     f.g = (int)div_small(r, per_head);
     r -= f.g * per_head;
     int lo = 0, hi = tile_count(a, s);
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (units_before(a, s, mid) <= r)
-            lo = mid;
-        else
-            hi = mid;
+    if (hi <= kFewTiles) {
+        for (int u; r >= (u = kTileCost + tile_blocks(a, s, lo)); ++lo) r -= u;
+    } else {
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (units_before(a, s, mid) <= r)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        r -= units_before(a, s, lo);
     }
     f.tile = lo;
-    f.off = (int)(r - units_before(a, s, lo));
+    f.off = (int)r;
     f.len = (int)cut.len(cta);
     f.first = cut.cta_of(cut.start(cta) - f.off + kTileCost);
     return f;
@@ -316,8 +328,12 @@ struct Piece {
 struct Walk {
     Run r;
     Seq s;
+    int tiles;
     DEC_HD Walk(const ChunkArgs& a, const Run& run) : r(run) {
-        if (r.len > 0) s = seq_of(a, r.b);
+        if (r.len > 0) {
+            s = seq_of(a, r.b);
+            tiles = tile_count(a, s);
+        }
     }
     DEC_HD bool next(const ChunkArgs& a, Piece* p) {
         while (r.len > 0)
@@ -344,12 +360,13 @@ struct Walk {
         r.len -= units;
         r.off = 0;
         if (r.len > 0) {  // the tile is done
-            if (++r.tile == tile_count(a, s)) {
+            if (++r.tile == tiles) {
                 r.tile = 0;
                 if (++r.g == a.nkv) {
                     r.g = 0;
                     do s = seq_of(a, ++r.b);
                     while (s.n == 0);
+                    tiles = tile_count(a, s);
                 }
             }
         }
@@ -568,7 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------- TMA producer
         const int pool_rows = a.n_pages * a.nkv * kPage;
         int item = 0, n = 0, nd = 0;  // ring items, pieces, blocks to be cleaned
-        bool was_two = false;
         bool ok = true;
         while (ok && walk.next(a, &pc)) {
             const int page_lo = pc.lo / kPage, page_hi = pc.hi / kPage;
@@ -581,11 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int have = 0, cur = entries(0), nxt = entries(1);
             const int LA = pc.two ? 1 : 2;
-            // Q may be loaded once the last piece's scores are done; where the last piece's result passes
-            // through a place that this piece's Q takes, once that piece is done
             if (n > 0 && !wait(&ctl.q_empty, (n - 1) & 1, err)) break;
-            if (n > 0 && (pc.two || was_two) && !wait(&ctl.o_free, (n - 1) & 1, err)) break;
-            was_two = pc.two;
             if (elected()) {
                 const int subs = pc.two ? 2 : 1;
                 mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(subs * a.tps * a.G * D * 2));
@@ -1042,11 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
             float* slot = a.ws + (size_t)(2 * blockIdx.x + (pc.starts ? 1 : 0)) * S::kSlotFloats +
                           (pc.two ? s * S::kSubFloats : 0);
-            // a warp's rows of the result pass through the place of Q: the sub-tile's own, done with, or for a
-            // joined result sub-tile 1's, not in use
-            const int cw = (c_hi - c_lo) / 8;  // 16-byte pieces of a row: 4, 8 or 16
-            uint4* stage = reinterpret_cast<uint4*>(smem + (pc.two ? s : 1) * S::kBlock) +
-                           (pc.two ? warp % kSubWarps : warp) * 32 * cw;
+            uint16_t* dst = a.out + ((size_t)(pc.row0 + tok) * a.nq + (size_t)pc.g * a.G + hh) * D;
 #pragma unroll 1
             for (int c0 = busy ? c_lo : c_hi; c0 < c_hi; c0 += 16) {
                 uint32_t o[16], o1[16];
@@ -1079,35 +1087,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 }
                             }
                 }
-                if (whole_tile) {
-                    // 16-byte pieces, permuted within the row so that 8 lanes use all banks
+                if (valid && ok) {
+                    if (whole_tile) {
+                        // a whole 32-byte sector of the thread's row
 #pragma unroll
-                    for (int q = 0; q < 16; q += 8) {
-                        uint4 y;
-                        y.x = pack_bf2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv);
-                        y.y = pack_bf2(__uint_as_float(o[q + 2]) * inv, __uint_as_float(o[q + 3]) * inv);
-                        y.z = pack_bf2(__uint_as_float(o[q + 4]) * inv, __uint_as_float(o[q + 5]) * inv);
-                        y.w = pack_bf2(__uint_as_float(o[q + 6]) * inv, __uint_as_float(o[q + 7]) * inv);
-                        stage[lane * cw + (((c0 - c_lo + q) / 8) ^ (lane & (cw - 1)))] = y;
+                        for (int q = 0; q < 16; q += 8) {
+                            uint4 y;
+                            y.x = pack_bf2(__uint_as_float(o[q]) * inv, __uint_as_float(o[q + 1]) * inv);
+                            y.y = pack_bf2(__uint_as_float(o[q + 2]) * inv, __uint_as_float(o[q + 3]) * inv);
+                            y.z = pack_bf2(__uint_as_float(o[q + 4]) * inv, __uint_as_float(o[q + 5]) * inv);
+                            y.w = pack_bf2(__uint_as_float(o[q + 6]) * inv, __uint_as_float(o[q + 7]) * inv);
+                            *reinterpret_cast<uint4*>(dst + c0 + q) = y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; q += 4)
+                            *reinterpret_cast<uint4*>(slot + ((size_t)((c0 + q) / 4) * kRows + r) * 4) =
+                                make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]);
                     }
-                } else if (valid && ok) {
-#pragma unroll
-                    for (int q = 0; q < 16; q += 4)
-                        *reinterpret_cast<uint4*>(slot + ((size_t)((c0 + q) / 4) * kRows + r) * 4) =
-                            make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]);
                 }
-            }
-            if (whole_tile && busy) {
-                // the rows leave by whole segments: cw lanes a row
-                const long long at = valid && ok ? ((long long)(pc.row0 + tok) * a.nq + (long long)pc.g * a.G + hh) * D + c_lo : -1;
-                __syncwarp();
-#pragma unroll 4
-                for (int i = lane; i < 32 * cw; i += 32) {
-                    const int row = i / cw, c = i & (cw - 1);
-                    const long long to = __shfl_sync(0xffffffffu, at, row);
-                    if (to >= 0) *reinterpret_cast<uint4*>(a.out + to + 8 * c) = stage[row * cw + (c ^ (row & (cw - 1)))];
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next Q goes there by TMA
             }
             if (valid && ok && !whole_tile && c_lo == 0) {
                 slot[kRows * D + r] = m;
