@@ -289,23 +289,30 @@ __global__ void __launch_bounds__(kApThreads, 4) paged_rope_append_kernel(Append
     if (a.q_norm) gq0 = *reinterpret_cast<const float4*>(a.q_norm + 4 * sub), gq1 = *reinterpret_cast<const float4*>(a.q_norm + H + 4 * sub);
     if (a.k_norm) gk0 = *reinterpret_cast<const float4*>(a.k_norm + 4 * sub), gk1 = *reinterpret_cast<const float4*>(a.k_norm + H + 4 * sub);
     int buf = 0;
+    // the values of the head in hand next: of this row, or after its last head of the next row
+    float4 x, y;
+    bool loaded = false;
+    auto load = [&](int t, int h) {
+        if (h >= heads) return;
+        const float* src = a.qkv + (size_t)t * a.ld + (size_t)h * D + 4 * sub;
+        if (a.aligned) {
+            x = __ldcs(reinterpret_cast<const float4*>(src));
+            y = __ldcs(reinterpret_cast<const float4*>(src + H));
+        } else {
+            x = make_float4(src[0], src[1], src[2], src[3]);
+            y = make_float4(src[H], src[H + 1], src[H + 2], src[H + 3]);
+        }
+    };
+    int next_slot = a.slot[blockIdx.x], next_p = a.row_pos[blockIdx.x];  // the grid has at most T blocks
     for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const int slot = a.slot[t], p = a.row_pos[t];
+        const int slot = next_slot, p = next_p;
+        if (t + (int)gridDim.x < a.T) {  // asked for a row ahead
+            next_slot = a.slot[t + gridDim.x];
+            next_p = a.row_pos[t + gridDim.x];
+        }
         if (slot < 0 || slot >= a.n_slots) continue;  // the whole block
-        const float* row = a.qkv + (size_t)t * a.ld;
-        // the first heads' values are on their way while the angles are worked out
-        float4 x, y;
-        auto load = [&](int h) {
-            const float* src = row + (size_t)h * D + 4 * sub;
-            if (a.aligned) {
-                x = __ldcs(reinterpret_cast<const float4*>(src));
-                y = __ldcs(reinterpret_cast<const float4*>(src + H));
-            } else {
-                x = make_float4(src[0], src[1], src[2], src[3]);
-                y = make_float4(src[H], src[H + 1], src[H + 2], src[H + 3]);
-            }
-        };
-        if (head0 < heads) load(head0);
+        if (!loaded) load(t, head0);
+        loaded = false;
         if (tid < H) {
             const double r = (double)p * turns, f = r - rint(r);
             float c, s;
@@ -319,7 +326,12 @@ __global__ void __launch_bounds__(kApThreads, 4) paged_rope_append_kernel(Append
         const size_t page = slot / kPage, off = slot % kPage;
         for (int h = head0; h < heads; h += kAtOnce) {
             float4 u = x, v = y;
-            if (h + kAtOnce < heads) load(h + kAtOnce);
+            if (h + kAtOnce < heads) {
+                load(t, h + kAtOnce);
+            } else if (t + (int)gridDim.x < a.T && next_slot >= 0 && next_slot < a.n_slots) {
+                load(t + gridDim.x, head0);
+                loaded = true;
+            }
             const bool isq = h < a.nq, isv = h >= a.nq + a.nkv;
             const int j = isq ? h : isv ? h - a.nq - a.nkv : h - a.nq;
             uint16_t* dst = isq ? a.q_out + ((size_t)t * a.nq + j) * D
