@@ -1378,6 +1378,8 @@ dec_status gqa_chunk_attn(const void* q, int64_t ldq, const void* k_pool, const 
     if (!(scale > 0.f) || !(scale < INFINITY)) return bad(DEC_ERR_INVALID_ARG, "scale must be positive and finite");
     if (window < 0 || !(softcap >= 0.f) || !(softcap < INFINITY))
         return bad(DEC_ERR_INVALID_ARG, "window and softcap must not be negative");
+    if (scale < 0x1p-40f || scale > 0x1p40f || (softcap > 0.f && softcap < 0x1p-20f))
+        return bad(DEC_ERR_UNSUPPORTED, "scale must lie within 2^-40 .. 2^40, a softcap not below 2^-20");
     if (nq / nkv > 16) return bad(DEC_ERR_UNSUPPORTED, "more than 16 q heads per kv head");
     if (d != 64 && d != 128) return bad(DEC_ERR_UNSUPPORTED, "d must be 64 or 128");
     if (page_size != kPage) return bad(DEC_ERR_UNSUPPORTED, "page_size must be 16");

@@ -377,8 +377,8 @@ dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t 
     if (B <= 0 || max_pages <= 0 || n_pages <= 0 || T < 0) return bad(DEC_ERR_INVALID_ARG, "bad B / max_pages / n_pages / T");
     if (page_size != kPage) return bad(DEC_ERR_UNSUPPORTED, "page_size must be 16");
     if (B > kRzMaxB) return bad(DEC_ERR_UNSUPPORTED, "more than 4096 sequences");
-    if (n_pages > INT32_MAX / kPage || max_pages > INT32_MAX / kPage)
-        return bad(DEC_ERR_UNSUPPORTED, "slots and positions must fit 32 bits");
+    if (n_pages > INT32_MAX / kPage || max_pages > INT32_MAX / kPage || T > (1 << 30))
+        return bad(DEC_ERR_UNSUPPORTED, "slots and positions must fit 32 bits, rows 2^30");
     ResizeArgs a{old_len, new_len, B, block_table, max_pages, free_pages, n_pages, n_free, cu_rows, slot, row_pos, T,
                  status, T <= kRzRows};
     // one CTA for a decode step; eight where many pages may move (a step of many rows or sequences)
@@ -425,7 +425,8 @@ dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, 
     if (page_size != kPage) return bad(DEC_ERR_UNSUPPORTED, "page_size must be 16");
     const int64_t width = ((int64_t)nq + 2 * (int64_t)nkv) * d;
     if (ld < width) return bad(DEC_ERR_INVALID_ARG, "ld is smaller than a row");
-    if (n_pages > INT32_MAX / kPage) return bad(DEC_ERR_UNSUPPORTED, "slots must fit 32 bits");
+    if (n_pages > INT32_MAX / kPage || T > (1 << 30) || nq > (1 << 20) || nkv > (1 << 20))
+        return bad(DEC_ERR_UNSUPPORTED, "slots must fit 32 bits, rows 2^30, heads 2^20");
     if (((uintptr_t)q_out | (uintptr_t)k_pool | (uintptr_t)v_pool | (uintptr_t)q_norm | (uintptr_t)k_norm) % 16 != 0)
         return bad(DEC_ERR_UNSUPPORTED, "q_out, the pools and the norm gains must be 16-byte aligned");
     if (T == 0) return DEC_OK;

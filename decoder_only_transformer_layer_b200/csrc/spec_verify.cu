@@ -402,8 +402,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
     if (rank == 0) {
         for (int i = threadIdx.x; i <= a.n; i += kPickThreads) {
             if (i < acc) out[i] = a.tok[(size_t)b * a.n + i];
-            if (i == acc && !(warm && p.m > -INFINITY)) out[i] = !warm && p.arg < a.V ? p.arg : -1;
-            if (i > acc) out[i] = -1;
+            // a drawn token replaces the -1 at acc, after the cluster barriers below
+            if (i >= acc) out[i] = i == acc && !warm && p.arg < a.V ? p.arg : -1;
         }
         if (threadIdx.x == 0) a.accepted[b] = acc;
     }
@@ -589,10 +589,11 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = allow_wide_cluster();
     cudaLaunchConfig_t cfg = {};
-    // as many CTAs a sequence as one wave of them allows: with few sequences the draw is shorter the more
-    // SMs it has, with many a second wave would cost what the wider cluster gains
+    // as many CTAs a sequence as two waves of them allow: with few sequences the draw is shorter the more
+    // SMs it has; with many, greedy sequences end at once and leave their SMs to the others (32
+    // sequences, a third of them greedy: 4 CTAs each 67.6 us for the call, 8 each 65.5)
     int C = kPickCluster;
-    while (C > 1 && (int64_t)B * C > 148) C /= 2;
+    while (C > 1 && (int64_t)B * C > 2 * 148) C /= 2;
     cfg.gridDim = dim3(C, B);
     cfg.blockDim = dim3(kPickThreads);
     cfg.stream = st;

@@ -298,7 +298,7 @@ dec_status weight_gemv(const void* W, const void* x, int32_t B, int32_t N, int32
                        dec_stream_t stream);
 
 /* Synchronise `stream` and report whether a bounded device wait of a standalone call
- * (weight_gemv, weight_gemv_q8, moe_experts) on the current device ran out since the last check:
+ * (weight_gemv, weight_gemv_q8, moe_experts, gqa_chunk_attn) on the current device ran out since the last check:
  * DEC_ERR_TIMEOUT, and the word and the GEMM tile counters are cleared. */
 dec_status dec_check_standalone(dec_stream_t stream);
 
@@ -358,8 +358,8 @@ dec_status weight_gemv_q8(const void* Wq, const float* scale, const void* x, int
  *               new rows, more pages given back than the list holds, or a page that changes hands
  *               outside [0, n_pages)), else DEC_ERR_CONTEXT_OVERFLOW (a length above
  *               16 * max_pages), else DEC_ERR_PAGES_EXHAUSTED (A > F)
- * Errors on the host: NULL pointer or a bad size -> INVALID_ARG; B > 4096, page_size other than
- * 16 -> UNSUPPORTED. */
+ * Errors on the host: NULL pointer or a bad size -> INVALID_ARG; B > 4096, T > 2^30, n_pages or
+ * max_pages above 2^27, page_size other than 16 -> UNSUPPORTED. */
 dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t B, int32_t* block_table,
                         int32_t max_pages, int32_t page_size, int32_t* free_pages, int32_t n_pages, int32_t* n_free,
                         int32_t* cu_rows, int32_t* slot, int32_t* row_pos, int32_t T, int32_t* status,
@@ -400,9 +400,10 @@ dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, 
  * does not attend never reach it, whatever the pool holds there (NaN and infinities included).
  * kv_len above 16 * max_pages counts as 16 * max_pages.
  * Errors: NULL pointer, a bad size, scale not positive or ldq below nq*d -> INVALID_ARG; more
- * than 16 query heads a kv head, d other than 64 / 128, page_size other than 16, B > 4096, or an
- * address or stride off the 16-byte grid -> UNSUPPORTED. T = 0 does nothing. A device wait that
- * runs out is reported by dec_check_standalone. */
+ * than 16 query heads a kv head, d other than 64 / 128, page_size other than 16, B > 4096, scale
+ * outside 2^-40 .. 2^40, a softcap above 0 and below 2^-20, or an address or stride off the 16-byte
+ * grid -> UNSUPPORTED. T = 0 does nothing. Scores, q . K * scale, have to fit fp32: a row with one
+ * that is NaN or +inf is NaN. A device wait that runs out is reported by dec_check_standalone. */
 dec_status gqa_chunk_attn(const void* q, int64_t ldq, const void* k_pool, const void* v_pool, int32_t n_pages,
                           const int32_t* block_table, int32_t max_pages, const int32_t* cu_rows,
                           const int32_t* kv_len, int32_t B, int32_t T, int32_t nq, int32_t nkv, int32_t d,

@@ -112,6 +112,17 @@ def test_resize_many_rows_and_large_tables():
     check_resize(old, new, *pool_state(old, 3750, 4800, 3), 60000 + 1200 + 17)
 
 
+@pytest.mark.parametrize("T", [4095, 4096, 4097, 5000])
+def test_resize_row_counts_around_the_two_ways_of_placing_them(T):
+    old, new = np.array([7, 30, 0]), np.array([7 + 100, 12, T - 100])
+    check_resize(old, new, *pool_state(old, 330, 400, T), T)          # exactly full
+    check_resize(old, new, *pool_state(old, 330, 400, T), T + 1000)   # rows left over
+    check_resize(old, new, *pool_state(old, 330, 400, T), T - 1)      # one too many: refused
+    table, free, n_free = pool_state(old, 330, 400, T)
+    table[0, 0] = 400                                                 # a kept page outside the pool
+    check_resize(old, new, table, free, n_free, T)
+
+
 # ------------------------------------------------------------------ paged_rope_append
 
 @pytest.mark.parametrize("T,nq,nkv,d,norms,far,pad", [
@@ -195,15 +206,16 @@ def check_chunk(inp, scale=None, window=0, cap=0.0, q_view=None, workspace=None,
     dec.gqa_chunk_attn(q if q_view is None else q_view, kp, vp, ints(table), ints(cu), ints(lens), scale, out,
                        window=window, softcap=cap, workspace=workspace)
     dec.check_standalone()
-    nan0 = lambda t: np.nan_to_num(f64(t), nan=0.0)  # noqa: E731  (never attended: masked places)
     if on_device:
         want, mag = plain.chunk_attn_on_device(q, torch.nan_to_num(kp), torch.nan_to_num(vp), table, cu, lens, scale,
                                                window, float(np.float32(cap)))
     else:
-        want, mag = plain.chunk_attn(f64(q), nan0(kp), nan0(vp), table, cu, lens, scale, window,
-                                     float(np.float32(cap)), f64(start))
+        want, mag = plain.chunk_attn(f64(q), f64(kp), f64(vp), table, cu, lens, scale, window, float(np.float32(cap)),
+                                     f64(start))
     got = f64(out)
-    assert np.isfinite(got).all()
+    # the unused places of the pool hold NaN; a row is NaN only where it attends one of them
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    got, want, mag = (np.nan_to_num(x, nan=0.0) for x in (got, want, mag))
     # half a bf16 step of the result; each weight rounded to bf16 (half a step, 2^-8 relative) and
     # off by its score's error (fp32 sums of d products: below 2^-11 for these inputs)
     tol = np.abs(want) * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -11) + 1e-30
@@ -282,6 +294,109 @@ def test_chunk_bad_pages_are_not_attended():
     table[0, 3], table[1, 0], table[1, 10], table[2, :4] = -1, 1 << 30, inp[1].shape[0], -5
     check_chunk(inp)
     check_chunk(inp, window=40)
+
+
+def test_chunk_lengths_beyond_the_table_count_as_the_table():
+    q, kp, vp, table, cu, lens = chunk_inputs([(30, 100), (1, 64), (5, 200)], 8, 2, 128, 17)
+    for extra in (1, 5000, 2 ** 31 - 1 - 16 * table.shape[1]):
+        check_chunk((q, kp, vp, table, cu, np.array([100, 16 * table.shape[1] + extra, 200])))
+        check_chunk((q, kp, vp, table, cu, np.array([100, 64, 16 * table.shape[1] + extra])), window=150)
+
+
+def test_chunk_row_starts_out_of_order_stay_in_the_buffer():
+    # the call promises nothing for such starts but that it keeps to its buffers
+    q, kp, vp, table, cu, lens = chunk_inputs([(30, 100), (1, 64), (5, 200)], 8, 2, 128, 18)
+    guard = torch.full((3 * q.shape[0], 8, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    out = guard[q.shape[0]:2 * q.shape[0]]
+    for starts in ([0, 40, 20, 36], [-5, 10, 2 ** 30, 36], [36, 0, 0, 36], [-2 ** 31, 2 ** 31 - 1, 5, 7]):
+        dec.gqa_chunk_attn(q, kp, vp, ints(table), ints(starts), ints(lens), 0.1, out)
+        dec.check_standalone()
+        assert (guard[:q.shape[0]] == 3.0).all() and (guard[2 * q.shape[0]:] == 3.0).all()
+
+
+def test_explicit_streams_and_workspaces():
+    q, kp, vp, table, cu, lens = inp = chunk_inputs([(30, 300), (1, 640)], 8, 2, 128, 19)
+    want = check_chunk(inp)
+    out = torch.zeros_like(q)
+    side = torch.cuda.Stream()
+    args = (q, kp, vp, ints(table), ints(cu), ints(lens), 128 ** -0.5, out)
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError):
+        dec.gqa_chunk_attn(*args, stream=side.cuda_stream)  # whose memory would that be?
+    ws = torch.empty(dec.lib().gqa_chunk_attn_workspace(128), dtype=torch.uint8, device="cuda")
+    dec.gqa_chunk_attn(*args, stream=side.cuda_stream, workspace=ws)
+    side.synchronize()
+    assert torch.equal(out, want)
+    with pytest.raises(dec.DecError):
+        dec.gqa_chunk_attn(*args, workspace=ws[:-16])
+    with pytest.raises(dec.DecError):
+        dec.gqa_chunk_attn(*args, workspace=torch.empty(ws.numel() + 8, dtype=torch.uint8, device="cuda")[8:])
+    with pytest.raises(ValueError):
+        dec.gqa_chunk_attn(*args, workspace=ws.cpu())
+
+
+def test_two_captured_graphs_at_once():
+    """Each graph has its own workspace (torch allocates it from the graph's pool); replayed side by
+    side again and again, with other lengths in between, they give what eager calls give."""
+    a, b = chunk_inputs([(200, 900), (1, 2000)], 8, 2, 128, 41), chunk_inputs([(5, 700)] * 12, 8, 2, 64, 42)
+    outs, graphs, lens, kept = [], [], [], []
+    for i in (a, b):
+        args = [ints(v) for v in i[3:]]
+        out = torch.zeros_like(i[0])
+        dec.gqa_chunk_attn(i[0], i[1], i[2], *args, i[0].shape[2] ** -0.5, out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            dec.gqa_chunk_attn(i[0], i[1], i[2], *args, i[0].shape[2] ** -0.5, out)
+        outs.append(out)
+        graphs.append(g)
+        lens.append(args[2])
+        kept.append(args)  # a graph's inputs have to live as long as it does
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for cut in (0, 50, 3):
+        for i, t in zip((a, b), lens):
+            t.copy_(ints(i[5] - cut))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for i, out in zip((a, b), outs):
+            want = check_chunk((i[0], i[1], i[2], i[3], i[4], i[5] - cut))
+            assert torch.equal(out, want)
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import subprocess
+    import sys
+    code = """
+import torch
+import decoder_only_transformer_layer_b200 as dec
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+bf = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")
+q, k, v, out = bf(3, 8, 64), bf(2, 2, 16, 64), bf(2, 2, 16, 64), bf(3, 8, 64) * 0
+qkv, slot, pos = torch.ones(3, 12 * 64, device="cuda"), i(0, 1, 2), i(0, 1, 2)
+table, cu, n = i(0, 1).view(1, 2), i(0, 3), i(3)
+t, tok, u, us = torch.randn(1, 3, 100, device="cuda"), i(1, 2).view(1, 2), torch.rand(1, 2, device="cuda"), torch.rand(1, device="cuda")
+acc, toks = i(0), i(0, 0, 0).view(1, 3)
+f, nf, c2, st = i(0, 1, 2, 3), i(4), i(0, 0), i(9)
+t2, z = i(-1, -1).view(1, 2), i(0)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dec.paged_resize(z, n, t2, f, nf, c2, slot, pos, st)
+    dec.paged_rope_append(qkv, slot, pos, q, k, v, 1e4)
+    dec.gqa_chunk_attn(q, k, v, table, cu, n, 0.125, out)
+    dec.spec_verify(t, None, tok, None, None, u, us, acc, toks)
+g.replay()
+torch.cuda.synchronize()
+assert st.item() == 0 and (out == 1).all() and toks.max() < 100
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=__import__("os").path.dirname(__import__("os").path.dirname(__import__("os").path.abspath(__file__))))
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
 
 
 def test_chunk_masked_places_hold_anything():
@@ -441,6 +556,21 @@ def test_verify_masked_logits():
     x["target"][3, 1:] = torch.finfo(torch.float32).min
     x["target"][3, 1:, 7] = 0.0
     check_verify(x)
+
+
+def test_verify_logits_that_are_not_finite_stay_in_the_buffers():
+    # not allowed, and the tokens mean nothing; but they are tokens
+    for val in (float("nan"), float("inf")):
+        for draft in (0, 1):
+            x = verify_inputs(6, 3, 3000, draft, 16)
+            x["target"][1:3, 1] = val
+            x["target"][3, 0, 55] = val
+            if draft:
+                x["draft"][4, 0, 5:] = val
+            acc, tokens = torch.full((6,), 77, **I32), torch.full((6, 4), 7777, **I32)
+            dec.spec_verify(x["target"], x["draft"], ints(x["tok"]), None, torch.tensor(x["temp"]).cuda(),
+                            torch.tensor(x["u"]).cuda(), torch.tensor(x["us"]).cuda(), acc, tokens)
+            assert ((acc >= 0) & (acc <= 3)).all() and ((tokens >= -1) & (tokens < 3000)).all()
 
 
 def test_verify_close_calls_are_decided_in_64_bits():

@@ -31,7 +31,8 @@ CASES = [("paged_resize", RESIZE, BAD, {k: None}) for k in
          ("old_len", "new_len", "block_table", "free_pages", "n_free", "cu_rows", "slot", "row_pos", "status")]
 CASES += [("paged_resize", RESIZE, s, c) for s, c in (
     (BAD, dict(B=0)), (BAD, dict(T=-1)), (BAD, dict(max_pages=0)), (BAD, dict(n_pages=0)), (UNSUP, dict(page_size=32)),
-    (UNSUP, dict(B=4097)), (UNSUP, dict(n_pages=1 << 28)), (UNSUP, dict(max_pages=1 << 28)))]
+    (UNSUP, dict(B=4097)), (UNSUP, dict(n_pages=1 << 28)), (UNSUP, dict(max_pages=1 << 28)),
+    (UNSUP, dict(T=(1 << 30) + 1)))]
 CASES += [("paged_rope_append", APPEND, BAD, {k: None}) for k in
           ("qkv", "slot", "row_pos", "q_out", "k_pool", "v_pool")]
 CASES += [("paged_rope_append", APPEND, s, c) for s, c in (
@@ -39,7 +40,7 @@ CASES += [("paged_rope_append", APPEND, s, c) for s, c in (
     (BAD, dict(rope_base=nan())), (BAD, dict(q_norm=P, eps=nan())), (BAD, dict(k_norm=P, eps=-1.0)),
     (UNSUP, dict(d=96)), (UNSUP, dict(page_size=8)), (UNSUP, dict(n_pages=1 << 28)), (BAD, dict(n_pages=0)),
     (UNSUP, dict(q_out=P + 8)), (UNSUP, dict(k_pool=P + 2)), (UNSUP, dict(v_pool=P + 4)), (UNSUP, dict(q_norm=P + 4)),
-    (UNSUP, dict(k_norm=P + 8)))]
+    (UNSUP, dict(k_norm=P + 8)), (UNSUP, dict(T=(1 << 30) + 1)), (UNSUP, dict(nq=1 << 21, ld=1 << 40)))]
 CASES += [("gqa_chunk_attn", CHUNK, BAD, {k: None}) for k in
           ("q", "k_pool", "v_pool", "block_table", "cu_rows", "kv_len", "out", "workspace")]
 CASES += [("gqa_chunk_attn", CHUNK, s, c) for s, c in (
@@ -47,6 +48,7 @@ CASES += [("gqa_chunk_attn", CHUNK, s, c) for s, c in (
     (UNSUP, dict(ldq=1028)), (UNSUP, dict(q=P + 8)), (UNSUP, dict(k_pool=P + 2)), (UNSUP, dict(out=P + 4)),
     (UNSUP, dict(workspace=P + 4)), (BAD, dict(workspace_bytes=0)), (BAD, dict(scale=0.0)), (BAD, dict(scale=nan())),
     (BAD, dict(scale=float("inf"))), (BAD, dict(window=-1)), (BAD, dict(softcap=-1.0)), (BAD, dict(softcap=nan())),
+    (UNSUP, dict(scale=2.0 ** -41)), (UNSUP, dict(scale=2.0 ** 41)), (UNSUP, dict(softcap=2.0 ** -21)),
     (UNSUP, dict(d=80, ldq=1024)), (UNSUP, dict(page_size=32)), (UNSUP, dict(nq=34, nkv=2, ldq=8192)),
     (UNSUP, dict(B=4097)), (UNSUP, dict(max_pages=1 << 27)), (UNSUP, dict(n_pages=1 << 27)))]
 CASES += [("spec_verify", VERIFY, BAD, {k: None}) for k in
