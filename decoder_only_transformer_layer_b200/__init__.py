@@ -351,6 +351,19 @@ def weight_gemv_q8(Wq, scale, x, y, stream=None):
 
 # ---------------------------------------------------------------------- a step over a caller's paged cache
 
+_dtypes = None
+
+
+def _types():
+    """(float32, bfloat16, int32) of torch, looked up once: these calls cost their caller a few
+    microseconds, and an import statement is one of them."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = (torch.float32, torch.bfloat16, torch.int32)
+    return _dtypes
+
+
 def _want(name, t, dtype, shape, rows=0):
     """Refuse a tensor of another type, shape or layout than the call takes: its address alone goes
     to the library. None in ``shape`` is any extent; with ``rows`` only that many last dimensions
@@ -374,6 +387,11 @@ def _want(name, t, dtype, shape, rows=0):
 def _fits(t, dtype, *shape):
     """The checks of _want for a contiguous tensor, without the reasons."""
     return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _is(t, dtype, dim):
+    """The same where the extents are any."""
+    return t.dtype is dtype and t.dim() == dim and t.is_contiguous()
 
 
 def _device(*tensors):
@@ -420,15 +438,17 @@ def paged_resize(old_len, new_len, block_table, free_pages, n_free, cu_rows, slo
     Device int32 tensors: old_len, new_len [B]; block_table [B][max_pages]; free_pages [n_pages];
     n_free [1]; out: cu_rows [B + 1], slot and row_pos [T], status [1] (a STATUS code: nothing
     but the outputs changed unless it is 0)."""
-    from torch import int32 as i32
-    _want("block_table", block_table, i32, (None, None))
+    _, _, i32 = _types()
+    if not (_is(block_table, i32, 2) and _is(free_pages, i32, 1) and _is(slot, i32, 1)):
+        _want("block_table", block_table, i32, (None, None))
+        _want("free_pages", free_pages, i32, (None,))
+        _want("slot", slot, i32, (None,))
     B, max_pages = block_table.shape
-    _want("free_pages", free_pages, i32, (None,))
-    _want("slot", slot, i32, (None,))
     T = slot.shape[0]
-    for name, t, n in (("old_len", old_len, B), ("new_len", new_len, B), ("n_free", n_free, 1),
-                       ("cu_rows", cu_rows, B + 1), ("row_pos", row_pos, T), ("status", status, 1)):
-        if not _fits(t, i32, n):
+    if not (_fits(old_len, i32, B) and _fits(new_len, i32, B) and _fits(n_free, i32, 1) and
+            _fits(cu_rows, i32, B + 1) and _fits(row_pos, i32, T) and _fits(status, i32, 1)):
+        for name, t, n in (("old_len", old_len, B), ("new_len", new_len, B), ("n_free", n_free, 1),
+                           ("cu_rows", cu_rows, B + 1), ("row_pos", row_pos, T), ("status", status, 1)):
             _want(name, t, i32, (n,))
     index = _device(old_len, new_len, block_table, free_pages, n_free, cu_rows, slot, row_pos, status)
     _launch(lib().paged_resize, index, stream, old_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(),
@@ -442,13 +462,16 @@ def paged_rope_append(qkv, slot, row_pos, q_out, k_pool, v_pool, rope_base, q_no
     """QK-norm, RoPE and cache append of QKV rows. Device tensors: qkv fp32 [T][(nq + 2 nkv) d]
     (rows may be strided); slot, row_pos int32 [T]; q_out bf16 [T][nq][d]; pools bf16
     [n_pages][nkv][page][d]; q_norm, k_norm fp32 [d] or None. Rows with a negative slot are skipped."""
-    from torch import bfloat16, float32, int32
-    _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
-    n_pages, nkv, _, d = k_pool.shape
-    if not _fits(v_pool, bfloat16, n_pages, nkv, page_size, d):
+    float32, bfloat16, int32 = _types()
+    if not (_is(k_pool, bfloat16, 4) and _is(q_out, bfloat16, 3)):
+        _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
+        _want("q_out", q_out, bfloat16, (None, None, None))
+    n_pages, nkv, page, d = k_pool.shape
+    T, nq, qd = q_out.shape
+    if page != page_size or qd != d or not _fits(v_pool, bfloat16, n_pages, nkv, page_size, d):
+        _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
         _want("v_pool", v_pool, bfloat16, (n_pages, nkv, page_size, d))
-    _want("q_out", q_out, bfloat16, (None, None, d))
-    T, nq, _ = q_out.shape
+        _want("q_out", q_out, bfloat16, (None, None, d))
     width = (nq + 2 * nkv) * d
     if not _fits(qkv, float32, T, width):
         _want("qkv", qkv, float32, (T, width), rows=1)
@@ -472,17 +495,20 @@ def gqa_chunk_attn(q, k_pool, v_pool, block_table, cu_rows, kv_len, scale, out, 
     [B][max_pages]; cu_rows int32 [B + 1]; kv_len int32 [B] (new rows included); out bf16
     [T][nq][d]. workspace: a byte tensor of gqa_chunk_attn_workspace(d), or None for one
     allocated by torch for the call on the current stream (a call on another stream brings its own)."""
-    from torch import bfloat16, int32
-    _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
-    n_pages, nkv, _, d = k_pool.shape
-    if not _fits(v_pool, bfloat16, n_pages, nkv, page_size, d):
+    _, bfloat16, int32 = _types()
+    if not (_is(k_pool, bfloat16, 4) and _is(block_table, int32, 2)):
+        _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
+        _want("block_table", block_table, int32, (None, None))
+    n_pages, nkv, page, d = k_pool.shape
+    B, max_pages = block_table.shape
+    if page != page_size or not _fits(v_pool, bfloat16, n_pages, nkv, page_size, d):
+        _want("k_pool", k_pool, bfloat16, (None, None, page_size, None))
         _want("v_pool", v_pool, bfloat16, (n_pages, nkv, page_size, d))
-    _want("q", q, bfloat16, (None, None, d), rows=2)
+    if not (_is(q, bfloat16, 3) and q.shape[2] == d):
+        _want("q", q, bfloat16, (None, None, d), rows=2)
     T, nq, _ = q.shape
     if not _fits(out, bfloat16, T, nq, d):
         _want("out", out, bfloat16, (T, nq, d))
-    _want("block_table", block_table, int32, (None, None))
-    B, max_pages = block_table.shape
     if not (_fits(cu_rows, int32, B + 1) and _fits(kv_len, int32, B)):
         _want("cu_rows", cu_rows, int32, (B + 1,))
         _want("kv_len", kv_len, int32, (B,))
@@ -503,22 +529,24 @@ def spec_verify(target, draft, draft_tok, n_draft, temperature, u_accept, u_samp
     temperature fp32 [B] or None (1; <= 0 is greedy); u_accept fp32 [B][n] and u_sample fp32 [B] in
     [0, 1); out: n_accepted int32 [B], tokens int32 [B][n + 1] (accepted drafts, the next token,
     -1). workspace as in gqa_chunk_attn (spec_verify_workspace(B, n, V) bytes)."""
-    from torch import float32, int32
-    _want("target", target, float32, (None, None, None), rows=1)
+    float32, _, int32 = _types()
+    if not _is(target, float32, 3):
+        _want("target", target, float32, (None, None, None), rows=1)
     B, n1, V = target.shape
     n = n1 - 1
     if n < 0:
         raise ValueError("target: needs a row after the last draft")
-    if draft is not None:
+    if draft is not None and not _fits(draft, float32, B, n, V):
         _want("draft", draft, float32, (B, n, V), rows=1)
-    for name, t, dtype, shape in (("draft_tok", draft_tok, int32, (B, n)), ("u_accept", u_accept, float32, (B, n)),
-                                  ("u_sample", u_sample, float32, (B,)), ("n_accepted", n_accepted, int32, (B,)),
-                                  ("tokens", tokens, int32, (B, n1))):
-        if not _fits(t, dtype, *shape):
+    if not (_fits(draft_tok, int32, B, n) and _fits(u_accept, float32, B, n) and _fits(u_sample, float32, B) and
+            _fits(n_accepted, int32, B) and _fits(tokens, int32, B, n1)):
+        for name, t, dtype, shape in (("draft_tok", draft_tok, int32, (B, n)), ("u_accept", u_accept, float32, (B, n)),
+                                      ("u_sample", u_sample, float32, (B,)), ("n_accepted", n_accepted, int32, (B,)),
+                                      ("tokens", tokens, int32, (B, n1))):
             _want(name, t, dtype, shape)
-    if n_draft is not None:
+    if n_draft is not None and not _fits(n_draft, int32, B):
         _want("n_draft", n_draft, int32, (B,))
-    if temperature is not None:
+    if temperature is not None and not _fits(temperature, float32, B):
         _want("temperature", temperature, float32, (B,))
     index = _device(target, draft, draft_tok, n_draft, temperature, u_accept, u_sample, n_accepted, tokens, workspace)
     L = lib()
