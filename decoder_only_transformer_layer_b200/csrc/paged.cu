@@ -395,8 +395,9 @@ dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t 
     at[0].val.clusterDim.x = C;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = C > 1 ? 1 : 0;  // one CTA is a cluster of its own without the attribute, and launches sooner
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, paged_resize_kernel, a);
+    cfg.numAttrs = 1;
     if (e == cudaSuccess && !a.rows_here) {
         cfg.gridDim = dim3((T + 255) / 256);
         cfg.blockDim = dim3(256);
