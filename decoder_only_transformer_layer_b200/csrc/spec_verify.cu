@@ -16,9 +16,11 @@
 // exponentials, sums and cumulative sums are in fp64. An acceptance whose two sides are
 // too close for the fp32 sums is decided again with fp64 sums.
 //
-// Measured (B200): 32 sequences of up to 7 drafts over 128256 tokens, 158 MB of rows that count (5.6 TB/s), take 63 us
-// on the device, 28 for the first kernel and 35 for the draw, whose passes in fp64 are latency and
-// arithmetic on 8 SMs a sequence; one sequence of 4 drafts 14 us. Weights kept in registers between the
+// Measured (B200): 32 sequences of up to 7 drafts over 128256 tokens, 158 MB of rows that count, take 61 us
+// on the device: 27 for the first kernel (5.8 TB/s) and 34 for the draw. For a rejected row that is two passes
+// of 8 us over both rows on 8 SMs, bound by instructions (25 for an exponential, half of them fp64, at 16 warps
+// an SM), and 6 us of cluster barriers and dependent reads. Loads two steps ahead and a table of 16 entries
+// without bank conflicts changed nothing. One sequence of 4 drafts takes 13.4 us. Weights kept in registers between the
 // two passes over a rejected row changed nothing (13.6 us either way).
 #include <cuda_runtime.h>
 #include <math.h>
@@ -218,8 +220,10 @@ __host__ __device__ inline int run_per_lane(int V, int C) {
 struct PickShared {
     Stat row[2 * kMaxDrafts + 1];
     int verdict[kMaxDrafts];         // of each draft: 1 accepted, 0 not, 2 too close for fp32 sums
-    double warp[2][kPickWarps];
-    double cta[2][kPickCluster];     // written by every CTA of the cluster
+    // of the last two sums, in turn (a CTA that stores to the next sum's place has seen all CTAs leave the
+    // one before the last, whose place it is)
+    double warp[2][2][kPickWarps];
+    double cta[2][2][kPickCluster];  // written by every CTA of the cluster
     double table[64];                // 2^(i / 64)
 };
 
@@ -230,34 +234,35 @@ DEC_DEVINL double warp_sum_d(double v) {
 }
 
 // The sums over the cluster of x and y (one value a thread), in a fixed order; also this
-// CTA's own warps' totals in sh.warp and every CTA's in sh.cta. Every thread of the cluster calls it.
-DEC_DEVINL double2 cluster_sum(PickShared& sh, double x, double y, int rank, int C) {
+// CTA's own warps' totals in sh.warp[at] and every CTA's in sh.cta[at], `at` another one at each call.
+// Every thread of the cluster calls it. A cluster barrier costs 1400 cycles here.
+DEC_DEVINL double2 cluster_sum(PickShared& sh, int at, double x, double y, int rank, int C) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     x = warp_sum_d(x);
     y = warp_sum_d(y);
-    cluster_sync();  // the last call's values have been read
     if (lane == 0) {
-        sh.warp[0][warp] = x;
-        sh.warp[1][warp] = y;
+        sh.warp[at][0][warp] = x;
+        sh.warp[at][1][warp] = y;
     }
     __syncthreads();
     if (warp < 2) {  // warp w sums kind w and hands it to CTA `lane`
         double t = 0.0;
-        for (int w = 0; w < kPickWarps; ++w) t += sh.warp[warp][w];
+        for (int w = 0; w < kPickWarps; ++w) t += sh.warp[at][warp][w];
         if (lane < C)
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dsmem_map(smem_u32(&sh.cta[warp][rank]), lane)), "d"(t)
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(dsmem_map(smem_u32(&sh.cta[at][warp][rank]), lane)),
+                         "d"(t)
                          : "memory");
     }
     cluster_sync();
     double2 t = make_double2(0.0, 0.0);
     for (int r = 0; r < C; ++r) {
-        t.x += sh.cta[0][r];
-        t.y += sh.cta[1][r];
+        t.x += sh.cta[at][0][r];
+        t.y += sh.cta[at][1][r];
     }
     return t;
 }
 
-__global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs a) {
     __shared__ PickShared sh;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;  // one cluster a sequence
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -267,6 +272,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
     const double c = warm ? 1.4426950408889634074 / (double)T : 0.0;  // e^(l / T) = 2^(c l)
     const float k = log2e_over(T);
     if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(threadIdx.x / 64.0);
+    // the matching wait comes before the first store to another CTA's shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
 
     // ---- the rows' statistics from their pieces, a warp a row
@@ -326,6 +333,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
         sh.verdict[i] = v;
     }
     __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    int at = 0;  // of the last cluster_sum
 
     // The vocabulary in runs of 32 E values, one a warp (E a multiple of 4): in step t of E / 4 lane l takes
     // values 128 t + 4 l .. + 3 of the run, so that a warp reads whole lines.
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
                 for (int i = 0; i < 4; ++i) y[i & 1] += e[i];
             }
         }
-        return cluster_sum(sh, x[0] + x[1], y[0] + y[1], rank, C);
+        return cluster_sum(sh, at ^= 1, x[0] + x[1], y[0] + y[1], rank, C);
     };
 
     // ---- the first draft that is not accepted
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) own[i & 1] += weight(ep[i], eq[i], j + i);
             }
-            total = cluster_sum(sh, own[0] + own[1], 0.0, rank, C).x;
+            total = cluster_sum(sh, at ^= 1, own[0] + own[1], 0.0, rank, C).x;
             if (total > 0.0 || plain) break;
             plain = true;
         }
@@ -446,8 +455,8 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
             return at;
         };
         double base = 0.0;
-        if (find(sh.cta[0], C, &base) == rank) {
-            const int w = find(sh.warp[0], kPickWarps, &base);
+        if (find(sh.cta[at][0], C, &base) == rank) {
+            const int w = find(sh.warp[at][0], kPickWarps, &base);
             const int per = E / 16 > 0 ? (E + 15) / 16 : 1;  // values a lane has of the run: 512 lanes, 32 E values
             const long long begin = (long long)(rank * kPickWarps + w) * 32 * E, end = min((long long)a.V, begin + 32 * E);
             const long long j = begin + (long long)threadIdx.x * per;
@@ -461,9 +470,9 @@ __global__ void __launch_bounds__(kPickThreads, 1) verify_pick_kernel(VerifyArgs
                 if (lane >= o) cum += y;
             }
             __syncthreads();  // sh.warp has been read
-            if (lane == 31) sh.warp[0][warp] = cum;
+            if (lane == 31) sh.warp[at][0][warp] = cum;
             __syncthreads();
-            if (find(sh.warp[0], kPickWarps, &base) == warp) {
+            if (find(sh.warp[at][0], kPickWarps, &base) == warp) {
                 const unsigned some = __ballot_sync(0xffffffffu, own > 0.0);
                 const unsigned hit = __ballot_sync(0xffffffffu, own > 0.0 && base + cum > goal);
                 if (lane == (hit ? __ffs(hit) - 1 : 31 - __clz(some))) {
@@ -561,9 +570,9 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = allow_wide_cluster();
     cudaLaunchConfig_t cfg = {};
-    // as many CTAs a sequence as two waves of them allow: with few sequences the draw is shorter the more
-    // SMs it has; with many, greedy sequences end at once and leave their SMs to the others (32
-    // sequences, a third of them greedy: 4 CTAs each 67.6 us for the call, 8 each 65.5)
+    // as many CTAs a sequence as can all be on the SMs, two each: with few sequences the draw is shorter the
+    // more SMs it has; with many, greedy sequences end at once and leave their SMs to the others (32 sequences,
+    // half of them greedy: 8 CTAs each 60.6 us for the call, 16 each 60.8, and 4 each 2 us more than 8)
     int C = kPickCluster;
     while (C > 1 && (int64_t)B * C > 2 * 148) C /= 2;
     cfg.gridDim = dim3(C, B);
