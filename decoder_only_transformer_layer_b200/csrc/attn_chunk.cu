@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     const uint32_t tO = tmem + 2 * kKeys;  // S/P of sub-tile s at tmem + 128 s, its O at tO + D s
+    pdl_wait();     // all of the above ran beside the last kernel in the stream
     pdl_trigger();
     const Run run = find_run(a, blockIdx.x, ctl.scratch);
     Walk walk(a, run);
@@ -1150,6 +1151,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) chunk_join_kernel(const Chunk
     __shared__ float red[2][kJoinWarps][32];
     const int last = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
+    pdl_trigger();
     const Join jn = reinterpret_cast<const Join*>(reinterpret_cast<const char*>(a.ws) - kJoinBytes)[last];
     if (jn.first < 0) return;
     const int np = last - jn.first + 1;
@@ -1269,18 +1271,21 @@ cudaError_t launch(const ChunkArgs& a, const void* q, int64_t ldq, const void* k
     const auto kernel = a.cap > 0.f ? chunk_attn_kernel<D, true> : chunk_attn_kernel<D, false>;
     cudaError_t e = ensure_smem(reinterpret_cast<const void*>(kernel), smem);
     if (e != cudaSuccess) return e;
-    kernel<<<kCtas, kThreads, smem, st>>>(tmQ, tmK, tmV, a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCtas, kJoinBlocks);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = dim3(kCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, tmQ, tmK, tmV, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(kCtas, kJoinBlocks);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, chunk_join_kernel<D>, a);
 }
 

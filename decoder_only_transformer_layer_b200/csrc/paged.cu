@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(kApThreads, 4) paged_rope_append_kernel(Append
     const int tid = threadIdx.x, sub = tid % LH, head0 = tid / LH;
     double turns = 0.0;  // theta_i / 2 pi
     if (tid < H) turns = pow((double)a.base, -2.0 * tid / D) * 0.15915494309189533577;
+    pdl_wait();     // the power above ran beside the last kernel in the stream
+    pdl_trigger();
     const int heads = a.nq + 2 * a.nkv;
     float4 gq0, gq1, gk0, gk1;
     if (a.q_norm) gq0 = *reinterpret_cast<const float4*>(a.q_norm + 4 * sub), gq1 = *reinterpret_cast<const float4*>(a.q_norm + H + 4 * sub);
@@ -439,11 +441,16 @@ dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, 
                  ((uintptr_t)qkv | (uintptr_t)(ld * 4)) % 16 == 0};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int grid = std::min(T, 148 * 4);
-    if (d == 128)
-        paged_rope_append_kernel<128><<<grid, kApThreads, 0, st>>>(a);
-    else
-        paged_rope_append_kernel<64><<<grid, kApThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kApThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, d == 128 ? paged_rope_append_kernel<128> : paged_rope_append_kernel<64>, a);
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("paged_rope_append: ") + cudaGetErrorString(e));
     return DEC_OK;
 } catch (const std::exception&) {

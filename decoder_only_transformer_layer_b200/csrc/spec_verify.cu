@@ -96,6 +96,7 @@ DEC_DEVINL Stat join(const Stat& x, const Stat& y, float k) {
 // one, where it does not begin or end on a vector), four at a time, with one move of its maximum
 // for the four.
 __global__ void __launch_bounds__(kStatThreads) verify_stats_kernel(VerifyArgs a) {
+    pdl_wait();
     pdl_trigger();
     const int rows = 2 * a.n + 1;
     const int b = blockIdx.y / rows, i = blockIdx.y - b * rows;
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
     // the matching wait comes before the first store to another CTA's shared memory
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pdl_wait();
+    pdl_trigger();
 
     // ---- the rows' statistics from their pieces, a warp a row
     for (int i = warp; i < 2 * a.n + 1; i += kPickWarps) {
@@ -566,10 +568,17 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     a.accepted = n_accepted;
     a.tokens = tokens;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    verify_stats_kernel<<<dim3(a.splits, B * (2 * n + 1)), kStatThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = allow_wide_cluster();
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.splits, B * (2 * n + 1));
+    cfg.blockDim = dim3(kStatThreads);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stats_kernel, a);
+    if (e == cudaSuccess) e = allow_wide_cluster();
     // as many CTAs a sequence as can all be on the SMs, two each: with few sequences the draw is shorter the
     // more SMs it has; with many, greedy sequences end at once and leave their SMs to the others (32 sequences,
     // half of them greedy: 8 CTAs each 60.6 us for the call, 16 each 60.8, and 4 each 2 us more than 8)
@@ -577,14 +586,9 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     while (C > 1 && (int64_t)B * C > 2 * 148) C /= 2;
     cfg.gridDim = dim3(C, B);
     cfg.blockDim = dim3(kPickThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = C;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
     if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, verify_pick_kernel, a);
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("spec_verify: ") + cudaGetErrorString(e));
