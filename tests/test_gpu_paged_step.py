@@ -367,6 +367,69 @@ def test_two_captured_graphs_at_once():
             assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("way", ["eager", "two streams", "captured"])
+def test_calls_that_read_what_the_last_one_wrote(way):
+    """Chains of calls, each reading what the kernel, copy or other stream's kernel just before it
+    writes, give the same bits as with a synchronisation after each."""
+    T, nq, nkv, d, n_pages = 320, 8, 2, 64, 40
+    rng = np.random.default_rng(5)
+    x = torch.tensor(rng.normal(size=(T, (nq + 2 * nkv) * d)), dtype=torch.float32, device="cuda")
+    table = ints(rng.permutation(n_pages).reshape(2, 20))
+    old, new, lens = ints([0, 0]), ints([300, 20]), ints([300, 20])
+    u, us = torch.rand(T // 4, 3, device="cuda"), torch.rand(T // 4, device="cuda")
+
+    def buffers():
+        bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+        z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+        return dict(qkv=x.clone(), q=bf(T, nq, d), k=bf(n_pages, nkv, 16, d), v=bf(n_pages, nkv, 16, d),
+                    a=bf(T, nq, d), b=bf(T, nq, d), table=torch.full_like(table, -1), free=table.flatten().clone(),
+                    n_free=ints([n_pages]), cu=z(3), slot=z(T), pos=z(T), status=z(1) + 9, tok=z(T // 4, 3),
+                    acc=z(T // 4), toks=z(T // 4, 4))
+
+    def chain(s, after, streams):
+        last = torch.cuda.current_stream()
+        for k in range(6):
+            st = streams[k % len(streams)] if streams else last
+            st.wait_stream(last)
+            with torch.cuda.stream(st):
+                dec.paged_resize(old, new, s["table"], s["free"], s["n_free"], s["cu"], s["slot"], s["pos"], s["status"])
+                after()
+                dec.paged_rope_append(s["qkv"], s["slot"], s["pos"], s["q"], s["k"], s["v"], 1e4)
+                after()
+                dec.gqa_chunk_attn(s["q"], s["k"], s["v"], s["table"], s["cu"], lens, 0.125, s["a"])
+                after()
+                dec.gqa_chunk_attn(s["a"], s["k"], s["v"], s["table"], s["cu"], lens, 0.125, s["b"])
+                after()
+                s["q"].copy_(s["b"])
+                after()
+                dec.gqa_chunk_attn(s["q"], s["k"], s["v"], s["table"], s["cu"], lens, 0.125, s["a"])
+                after()
+                s["qkv"][:, :nq * d].add_(s["a"].reshape(T, nq * d))  # the next rows and the logits
+                after()
+                dec.spec_verify(s["qkv"].view(T // 4, 4, -1), None, s["tok"], None, None, u, us, s["acc"], s["toks"])
+                after()
+                s["tok"].copy_(s["toks"][:, :3].clamp_min(0))
+                dec.paged_resize(new, old, s["table"], s["free"], s["n_free"], s["cu"], s["slot"], s["pos"], s["status"])
+                after()
+            last = st
+        torch.cuda.current_stream().wait_stream(last)
+
+    want, got = buffers(), buffers()
+    chain(want, torch.cuda.synchronize, None)
+    side = [torch.cuda.Stream() for _ in range(2)] if way != "eager" else None
+    if way == "captured":
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            chain(got, lambda: None, side)
+        g.replay()
+    else:
+        chain(got, lambda: None, side)
+    torch.cuda.synchronize()
+    assert want["status"].item() == 0 and want["toks"].max() > 0
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+
+
 def test_first_call_of_a_process_may_be_captured():
     import subprocess
     import sys
