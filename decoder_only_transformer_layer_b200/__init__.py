@@ -386,12 +386,12 @@ def _want(name, t, dtype, shape, rows=0):
 
 def _fits(t, dtype, *shape):
     """The checks of _want for a contiguous tensor, without the reasons."""
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+    return getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_contiguous()
 
 
 def _is(t, dtype, dim):
     """The same where the extents are any."""
-    return t.dtype is dtype and t.dim() == dim and t.is_contiguous()
+    return getattr(t, "dtype", None) is dtype and t.dim() == dim and t.is_contiguous()
 
 
 def _device(*tensors):

@@ -151,3 +151,20 @@ def test_plain_resize_back_restores_everything():
 def test_library_names_are_bound():
     for f in ("paged_resize", "paged_rope_append", "gqa_chunk_attn", "spec_verify"):
         assert getattr(dec.lib(), f).restype == C.c_int and f in dec.__all__
+
+
+def test_wrappers_name_a_missing_tensor():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    f = torch.zeros
+    pool = bf(5, 2, 16, 64)
+    calls = (
+        (dec.paged_resize, [i(2), i(2), i(2, 3), i(9), i(1), i(3), i(4), i(4), i(1)], range(9)),
+        (dec.paged_rope_append, [f(4, 512), i(4), i(4), bf(4, 4, 64), pool, pool, 1e4], range(6)),
+        (dec.gqa_chunk_attn, [bf(4, 4, 64), pool, pool, i(1, 4), i(2), i(1), 1.0, bf(4, 4, 64)], (0, 1, 2, 3, 4, 5, 7)),
+        (dec.spec_verify, [f(2, 4, 50), None, i(2, 3), None, None, f(2, 3), f(2), i(2), i(2, 4)], (0, 2, 5, 6, 7, 8)))
+    for call, args, needed in calls:
+        for k in needed:
+            for wrong in (None, [1, 2]):
+                with pytest.raises(TypeError, match="expected a torch tensor"):
+                    call(*args[:k], wrong, *args[k + 1:])
