@@ -573,6 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
     }
+    // All of the above ran beside the last kernel in the stream. TMEM is taken after the wait: that kernel
+    // may still be about to take its own on this SM, and would wait for this one.
+    pdl_wait();
     if (warp == kSoftWarps + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
                      "r"(512)
@@ -584,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem;
     const uint32_t tO = tmem + 2 * kKeys;  // S/P of sub-tile s at tmem + 128 s, its O at tO + D s
-    pdl_wait();     // all of the above ran beside the last kernel in the stream
     pdl_trigger();
     const Run run = find_run(a, blockIdx.x, ctl.scratch);
     Walk walk(a, run);
