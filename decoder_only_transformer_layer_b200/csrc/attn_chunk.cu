@@ -32,7 +32,7 @@
 //
 // Measured (B200, 6.56 TB/s copy, 1610 TFLOP/s cuBLAS). A prompt of 8192 rows, 32/8 heads of 128: 502 us,
 // 1,095 TFLOP/s; bound by each sub-tile's chain of scores, softmax and products, two of which overlap (tensor
-// cores and exponentials are busy 56% of the time). 32 sequences of 5-8 rows at 1000-8000 keys: 117 us, 5.3
+// cores and exponentials are busy 56% of the time). 32 sequences of 5-8 rows at 1000-8000 keys: 115 us, 5.4
 // TB/s; bound by the stream of K and V, and by starting and joining (6 and 8 us). 5 rows at 4096: 17 us of
 // latencies. Score blocks of 64 keys, two buffers a sub-tile, would overlap a sub-tile's scores with its own
 // products, but a product with N = 64 costs as much as one with N = 128 and every step's issue comes twice: 610 us.
