@@ -501,11 +501,13 @@ DEC_DEVINL void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, ui
         "r"(a), "r"(b_lo), "r"(idesc), "r"(accum), "n"(kDescHi)
         : "memory");
 }
-DEC_DEVINL void commit_if(uint32_t on, uint64_t* bar) {
+// Arrives on `bar` once all products issued before it are done. A commit covers what its own thread issued, and
+// the products are issued by the lane that elect.sync gives (the same one for the same mask, but which one it
+// is nobody promises), so that lane commits. Called by the whole warp.
+DEC_DEVINL void commit_elected(uint64_t* bar) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %0, 0;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(on),
-        "r"(smem_u32(bar))
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
 DEC_DEVINL uint32_t desc_lo(uint32_t saddr, uint32_t leading) { return (saddr >> 4) | (leading << 16); }
@@ -666,7 +668,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t id_s = idesc_tc<128, 128, false>();
         constexpr uint32_t id_o = idesc_tc<128, D, true>();
         const uint32_t sb = smem_u32(smem), tm = uniform(tmem);
-        const uint32_t one = lane == 0;
         int item = 0, n = 0;
         uint32_t p_par = 0;               // parity of p_full[s] in bit s
         bool ok = true;
@@ -725,8 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (ok && from[s] == 0 && to[s] > 0) issue_s(s, sk, true);
-                if (ok) commit_if(one, &ctl.empty[sk]);
-                if (ok && pc.nb == 1) commit_if(one, &ctl.q_empty);
+                if (ok) commit_elected(&ctl.empty[sk]);
+                if (ok && pc.nb == 1) commit_elected(&ctl.q_empty);
                 more = walk.next(a, &nx);
                 for (int j = 0; j < pc.nb && ok; ++j) {
                     take(&st);
@@ -739,13 +740,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!ok) break;
                             issue_o(s, st, j == from[s]);
                         }
-                        if (s == 1) commit_if(one, &ctl.empty[st]);
+                        if (s == 1) commit_elected(&ctl.empty[st]);
                         if (j + 1 < pc.nb) {
                             if (s == 0) take(&sk);
                             if (!ok) break;
                             if (j + 1 >= from[s] && j + 1 < to[s]) issue_s(s, sk, true);
-                            if (s == 1) commit_if(one, &ctl.empty[sk]);
-                            if (s == 1 && j + 2 == pc.nb) commit_if(one, &ctl.q_empty);
+                            if (s == 1) commit_elected(&ctl.empty[sk]);
+                            if (s == 1 && j + 2 == pc.nb) commit_elected(&ctl.q_empty);
                         }
                     }
                 }
@@ -754,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     take(&sk);
                     if (!ok) break;
                     issue_s(k, sk, false);
-                    commit_if(one, &ctl.empty[sk]);
-                    if (k + 1 == pc.nb) commit_if(one, &ctl.q_empty);
+                    commit_elected(&ctl.empty[sk]);
+                    if (k + 1 == pc.nb) commit_elected(&ctl.q_empty);
                 }
                 more = walk.next(a, &nx);
                 for (int k = 0; k < pc.nb && ok; ++k) {
@@ -765,13 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait_o();
                     if (!ok) break;
                     issue_o(s, st, k < 2);
-                    commit_if(one, &ctl.empty[st]);
+                    commit_elected(&ctl.empty[st]);
                     if (k + 2 < pc.nb) {
                         take(&sk);
                         if (!ok) break;
                         issue_s(s, sk, false);
-                        commit_if(one, &ctl.empty[sk]);
-                        if (k + 3 == pc.nb) commit_if(one, &ctl.q_empty);
+                        commit_elected(&ctl.empty[sk]);
+                        if (k + 3 == pc.nb) commit_elected(&ctl.q_empty);
                     }
                 }
             }
