@@ -267,16 +267,18 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
     __shared__ PickShared sh;
     const int rank = blockIdx.x, C = gridDim.x, b = blockIdx.y;  // one cluster a sequence
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(threadIdx.x / 64.0);
+    // the matching wait comes before the first store to another CTA's shared memory
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // Nothing that another kernel writes is read before this wait, the counts and temperatures among it: that the
+    // first kernel has waited for whoever wrote them makes them visible to that kernel, not to this one.
+    pdl_wait();
+    pdl_trigger();
     const int nb = drafts_of(a, b);
     const float T = a.temp ? a.temp[b] : 1.f;
     const bool warm = T > 0.f;
     const double c = warm ? 1.4426950408889634074 / (double)T : 0.0;  // e^(l / T) = 2^(c l)
     const float k = log2e_over(T);
-    if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(threadIdx.x / 64.0);
-    // the matching wait comes before the first store to another CTA's shared memory
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    pdl_wait();
-    pdl_trigger();
 
     // ---- the rows' statistics from their pieces, a warp a row
     for (int i = warp; i < 2 * a.n + 1; i += kPickWarps) {

@@ -1,0 +1,50 @@
+"""The paged step's operators at the ends of what their documentation allows."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import _paged_plain as plain
+import decoder_only_transformer_layer_b200 as dec
+from test_gpu_paged_step import I32, check_chunk, check_verify, chunk_inputs, f64, ints, verify_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ spec_verify
+
+def run_verify(x):
+    """(accepted, tokens) of the inputs of verify_inputs."""
+    B, n1, _ = x["target"].shape
+    acc, tokens = torch.full((B,), 77, **I32), torch.full((B, n1), 77, **I32)
+    dev = lambda v: None if v is None else torch.tensor(v, device="cuda")  # noqa: E731
+    dec.spec_verify(x["target"], x["draft"], ints(x["tok"]), None if x["count"] is None else ints(x["count"]),
+                    dev(x["temp"]), dev(x["u"]), dev(x["us"]), acc, tokens)
+    return acc.cpu().numpy(), tokens.cpu().numpy()
+
+
+def test_verify_temperatures_and_counts_written_just_before_the_call():
+    x = verify_inputs(40, 4, 9001, 1, 51)
+    rng = np.random.default_rng(51)
+    sets = [(torch.tensor(rng.choice([0.0, 0.3, 1.0, 2.0], 40).astype(np.float32)).cuda(), ints(rng.integers(0, 5, 40)))
+            for _ in range(8)]
+    temp, count = torch.ones(40, device="cuda"), torch.zeros(40, **I32)
+    rest = (torch.tensor(x["u"]).cuda(), torch.tensor(x["us"]).cuda())
+    tok = ints(x["tok"])
+
+    def call(t, c, after):
+        acc, tokens = torch.zeros(40, **I32), torch.zeros((40, 5), **I32)
+        temp.copy_(t)
+        count.copy_(c)
+        after()
+        dec.spec_verify(x["target"], x["draft"], tok, count, temp, *rest, acc, tokens)
+        return acc, tokens
+
+    want = [call(t, c, torch.cuda.synchronize) for t, c in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [call(t, c, lambda: None) for t, c in sets]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
