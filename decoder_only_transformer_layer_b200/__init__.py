@@ -104,6 +104,7 @@ def lib():
         L.dec_check_standalone.argtypes = [_P]
         L.dec_test_fail_alloc.argtypes = [_I]
         L.dec_test_gemm_wait.argtypes = [_I, C.c_int64]
+        L.dec_test_chunk_wait.argtypes = [_I]
         L.dec_test_streamk_check.argtypes = [_I, _I, _I, _I]
         L.dec_test_streamk_check.restype = C.c_int
         L.dec_test_chunk_split.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I]
@@ -111,7 +112,7 @@ def lib():
         for f in ("dec_init", "dec_free", "dec_reset", "dec_prefill", "dec_step", "dec_last_argmax", "dec_kv_read",
                   "dec_kv_write", "dec_last_routes", "dec_last_hidden", "dec_seq_len", "gqa_decode_attn",
                   "gqa_decode_attn_noalloc", "moe_route_topk", "moe_experts", "weight_gemv", "dec_check",
-                  "dec_check_standalone", "dec_test_fail_alloc", "dec_test_gemm_wait", "dec_verify", "dec_truncate", "weight_gemv_q8", "ffn_gate_up",
+                  "dec_check_standalone", "dec_test_fail_alloc", "dec_test_gemm_wait", "dec_test_chunk_wait", "dec_verify", "dec_truncate", "weight_gemv_q8", "ffn_gate_up",
                   "paged_resize", "paged_rope_append", "gqa_chunk_attn", "spec_verify"):
             getattr(L, f).restype = C.c_int
         _lib = L
@@ -590,3 +591,9 @@ def test_gemm_wait(extra_pieces: int, limit_cycles: int):
     """Test hook: later tensor-core GEMM launches wait for pieces that never arrive and give
     up after limit_cycles; (0, 0) restores normal operation."""
     _check(lib().dec_test_gemm_wait(int(extra_pieces), int(limit_cycles)))
+
+
+def test_chunk_wait(kind: int):
+    """Test hook: in later gqa_chunk_attn calls the barriers of one kind (1 .. 10, as dec_api.h lists
+    them) never complete; 0 restores normal operation."""
+    _check(lib().dec_test_chunk_wait(int(kind)))

@@ -51,6 +51,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <exception>
 #include <string>
 
@@ -79,6 +80,7 @@ struct Int {
     static constexpr int value = N;
 };
 constexpr int kDirty = 8;      // more than the V blocks a ring holds
+constexpr long long kLimit = 1ll << 31;  // cycles after which a wait gives up
 constexpr int kPoison = 8;     // masked blocks a tile can have: at most 3 on its diagonal and 3 at its window's edge
 
 __device__ int g_chunk_err;    // a bounded wait ran out
@@ -112,7 +114,9 @@ struct ChunkArgs {
     const uint16_t* v_pool;
     uint16_t* out;
     float* ws;
+    int stall;  // test hook: this kind of barrier (Stall) never completes
 };
+enum Stall { kNoStall, kQFull, kQEmpty, kFull, kEmpty, kDirtyBar, kSFull, kPFull, kPvDone, kOFree, kCleanDone, kStalls };
 
 // A tile's last run says how to join it (one entry a CTA, at the start of the workspace).
 struct Join {
@@ -398,9 +402,13 @@ struct Control {
     uint64_t full[10], empty[10];
     uint64_t dirty[kDirty]; // loads of V blocks to be cleaned, in their order; the cleaning completes full[stage]
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t o_free;       // the epilogue has read O: 16 warps
+    uint64_t o_free;       // the epilogue has read O: 8 warps
     uint64_t clean_done;   // a piece's notes are complete: 2 warps
+    uint64_t drain;        // after a failure: every product issued is done
     uint32_t tmem;
+    int failed;            // a wait of this CTA gave up
+    int qs;                // pieces whose Q is loaded or on its way
+    uint32_t sent[10];     // of each place in the ring the last load's barrier (shared address) and phase parity; 0: none
     Poison poison;
     union {
         long long scratch[64];
@@ -420,9 +428,12 @@ DEC_DEVINL bool named_bar_and(uint32_t id, uint32_t n, bool v) {
     return r != 0;
 }
 
-// As mbar_wait_bounded, letting the hardware suspend the thread for up to 20 us at a time: a warp
-// that polls takes issue slots from the others.
-DEC_DEVINL bool wait(uint64_t* bar, uint32_t parity, int* err) {
+// A bounded wait (2^31 cycles, about a second), letting the hardware suspend the thread for up to 20 us at a time: a
+// warp that polls takes issue slots from the others. Every lane has its own answer, so no control flow that leads to a
+// warp-wide instruction depends on it: after a failure a warp walks on to the end of its run without waiting again, and
+// only what its lanes issue and store is left out. The loop is kept as small as it can be: looking at the clock
+// only every 32nd time takes a prompt of 8192 rows from 573 to 597 us (more polls), a vote over the warp to 619.
+DEC_DEVINL bool wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
     auto test = [&]() {
         uint32_t done;
         asm volatile(
@@ -436,8 +447,8 @@ DEC_DEVINL bool wait(uint64_t* bar, uint32_t parity, int* err) {
     if (test()) return true;
     const long long t0 = clock64();
     while (!test()) {
-        if (clock64() - t0 > (1ll << 32)) {
-            atomicExch(err, 1);
+        if (clock64() - t0 > kLimit) {
+            *failed = 1;
             return false;
         }
     }
@@ -501,13 +512,14 @@ DEC_DEVINL void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, ui
         "r"(a), "r"(b_lo), "r"(idesc), "r"(accum), "n"(kDescHi)
         : "memory");
 }
-// Arrives on `bar` once all products issued before it are done. A commit covers what its own thread issued, and
-// the products are issued by the lane that elect.sync gives (the same one for the same mask, but which one it
-// is nobody promises), so that lane commits. Called by the whole warp.
-DEC_DEVINL void commit_elected(uint64_t* bar) {
+// Arrives on `bar` once all products issued before it are done, if the issuing lane is `ok`. A commit covers what its
+// own thread issued, and the products are issued by the lane that elect.sync gives (the same one for the same mask,
+// but which one it is nobody promises), so that lane commits. Called by the whole warp.
+DEC_DEVINL void commit_elected(uint64_t* bar, bool ok) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        "{\n\t.reg .pred e, o;\n\tsetp.ne.u32 o, %1, 0;\n\telect.sync _|e, 0xffffffff;\n\tand.pred e, e, o;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"((uint32_t)ok)
         : "memory");
 }
 DEC_DEVINL uint32_t desc_lo(uint32_t saddr, uint32_t leading) { return (saddr >> 4) | (leading << 16); }
@@ -542,6 +554,21 @@ DEC_DEVINL float tanh_exact(float y) {
     return y2 < 0.0625f ? small : big;
 }
 
+// After a failure: shared memory and TMEM go to the next CTA only when nothing is in flight into them. Called by the MMA
+// warp, which waits for the products it issued, the last loads into the ring (at most one a stage) and the last Q.
+// Out of line: inside the kernel it costs every call 0.2 us.
+__device__ __noinline__ void drain(Control& ctl, int stages) {
+    volatile int* failed = &ctl.failed;
+    if ((threadIdx.x & 31) == 0) atomicExch(&g_chunk_err, 1);
+    commit_elected(&ctl.drain, true);
+    bool in = wait(&ctl.drain, 0, failed);
+    for (int i = 0; in && i < stages; ++i)
+        if (const uint32_t at = ctl.sent[i])
+            in = wait(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(at & ~1u)), at & 1, failed);
+    if (in && ctl.qs > 0) wait(&ctl.q_full, (ctl.qs - 1) & 1, failed);
+    __syncwarp();
+}
+
 template <int D, bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -551,24 +578,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& ctl = *reinterpret_cast<Control*>(smem + S::kOffCtl);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int* err = &g_chunk_err;
+    volatile int* failed = &ctl.failed;
 
     if (threadIdx.x == 0) {
-        mbar_init(&ctl.q_full, 1);
-        mbar_init(&ctl.q_empty, 1);
+        auto init = [&](uint64_t* bar, int arrivals, Stall kind) {
+            mbar_init(bar, arrivals + (a.stall == kind ? 1 << 16 : 0));
+        };
+        init(&ctl.q_full, 1, kQFull);
+        init(&ctl.q_empty, 1, kQEmpty);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&ctl.full[i], 1);
-            mbar_init(&ctl.empty[i], 1);
+            init(&ctl.full[i], 1, kFull);
+            init(&ctl.empty[i], 1, kEmpty);
         }
-        for (int i = 0; i < kDirty; ++i) mbar_init(&ctl.dirty[i], 1);
+        for (int i = 0; i < kDirty; ++i) init(&ctl.dirty[i], 1, kDirtyBar);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl.s_full[i], 1);
-            mbar_init(&ctl.p_full[i], kSubWarps);
-            mbar_init(&ctl.pv_done[i], 1);
+            init(&ctl.s_full[i], 1, kSFull);
+            init(&ctl.p_full[i], kSubWarps, kPFull);
+            init(&ctl.pv_done[i], 1, kPvDone);
         }
-        mbar_init(&ctl.o_free, kSoftWarps);
-        mbar_init(&ctl.clean_done, 2);
+        init(&ctl.o_free, kSoftWarps, kOFree);
+        init(&ctl.clean_done, 2, kCleanDone);
+        mbar_init(&ctl.drain, 1);
         fence_mbar_init();
+        ctl.failed = ctl.qs = 0;
+        for (int i = 0; i < kStages; ++i) ctl.sent[i] = 0;
     }
     if (warp == kSoftWarps && lane == 0) {
         prefetch_tmap(&tmQ);
@@ -601,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pool_rows = a.n_pages * a.nkv * kPage;
         int item = 0, n = 0, nd = 0;  // ring items, pieces, blocks to be cleaned
         bool ok = true;
-        while (ok && walk.next(a, &pc)) {
+        while (walk.next(a, &pc)) {
             const int page_lo = pc.lo / kPage, page_hi = pc.hi / kPage;
             const int32_t* tab = a.table + (size_t)pc.b * a.max_pages;
             // The lanes hold the table entries of four blocks (lane 8 i + p: page p of block 4 q + i), the next
@@ -612,9 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int have = 0, cur = entries(0), nxt = entries(1);
             const int LA = pc.two ? 1 : 2;
-            if (n > 0 && !wait(&ctl.q_empty, (n - 1) & 1, err)) break;
-            if (elected()) {
+            if (n > 0) ok = ok && wait(&ctl.q_empty, (n - 1) & 1, failed);
+            if (elected() && ok) {
                 const int subs = pc.two ? 2 : 1;
+                ctl.qs = n + 1;
                 mbar_arrive_expect_tx(&ctl.q_full, (uint32_t)(subs * a.tps * a.G * D * 2));
                 for (int s = 0; s < subs; ++s)
                     for (int h = 0; h < D / 64; ++h)
@@ -624,12 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             auto load = [&](const CUtensorMap* tm, int k, bool clean) {
                 const int st = item % kStages;
-                if (item >= kStages && !wait(&ctl.empty[st], (item / kStages - 1) & 1, err)) {
-                    ok = false;
-                    return;
-                }
+                if (item >= kStages) ok = ok && wait(&ctl.empty[st], (item / kStages - 1) & 1, failed);
+                uint64_t* bar = clean ? &ctl.dirty[nd % kDirty] : &ctl.full[st];
+                const uint32_t phase = clean ? nd / kDirty : item / kStages;
                 ++item;
-                uint64_t* bar = clean ? &ctl.dirty[nd++ % kDirty] : &ctl.full[st];
+                nd += clean;
                 const int first = (pc.kb0 + k) * (kKeys / kPage);  // the block's pages that hold keys of the tile
                 const int p0 = max(page_lo - first, 0), p1 = min(page_hi - first, kKeys / kPage - 1);
                 const int pg = (k >> 2) == have ? cur : nxt;
@@ -639,7 +672,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kKeys / kPage; ++i) y[i] = uniform(lane == (k & 3) * 8 + i ? row : 0u);
                 uint8_t* dst = smem + S::kOffRing + st * S::kBlock;
-                if (elected()) {
+                if (elected() && ok) {
+                    ctl.sent[st] = smem_u32(bar) | (phase & 1);
                     mbar_arrive_expect_tx(bar, (uint32_t)((p1 - p0 + 1) * kPage * D * 2));
 #pragma unroll
                     for (int i = 0; i < kKeys / kPage; ++i)
@@ -651,14 +685,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
             load(&tmK, 0, false);
-            if (ok && LA == 2 && pc.nb > 1) load(&tmK, 1, false);
-            for (int k = 0; k < pc.nb && ok; ++k) {
+            if (LA == 2 && pc.nb > 1) load(&tmK, 1, false);
+            for (int k = 0; k < pc.nb; ++k) {
                 if ((k >> 2) != have) {
                     cur = nxt;
                     nxt = entries(++have + 1);
                 }
                 load(&tmV, k, pc.masked(a, pc.kb0 + k));
-                if (ok && k + LA < pc.nb) load(&tmK, k + LA, false);
+                if (k + LA < pc.nb) load(&tmK, k + LA, false);
             }
             ++n;
         }
@@ -673,14 +707,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto take = [&](int* st) {        // the next ring item, loaded
             *st = item % kStages;
-            ok = ok && wait(&ctl.full[*st], (item / kStages) & 1, err);
+            ok = ok && wait(&ctl.full[*st], (item / kStages) & 1, failed);
             ++item;
         };
         auto issue_s = [&](int s, int st, bool two) {
             const uint32_t q = uniform(desc_lo(sb + (two ? s : 0) * S::kBlock, 1));
             const uint32_t k = uniform(desc_lo(sb + S::kOffRing + st * S::kBlock, 1));
             tc_fence_after();
-            if (elected()) {
+            if (elected() && ok) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t at = (kk >> 2) * (16384 >> 4) + (kk & 3) * (32 >> 4);
@@ -691,14 +725,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         };
         auto wait_p = [&](int s) {
-            ok = ok && wait(&ctl.p_full[s], (p_par >> s) & 1, err);
+            ok = ok && wait(&ctl.p_full[s], (p_par >> s) & 1, failed);
             p_par ^= 1u << s;
         };
         auto issue_o = [&](int s, int st, bool first) {
             const uint32_t v = uniform(desc_lo(sb + S::kOffRing + st * S::kBlock, 16384 >> 4));
             const uint32_t d = tm + 2 * kKeys + s * D, p = tm + s * kKeys, more = uniform(first ? 0u : 1u);
             tc_fence_after();
-            if (elected()) {
+            if (elected() && ok) {
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     mma_ts(d, p + kk * 8, v + kk * (2048 >> 4), id_o, kk > 0 ? 1u : more);
@@ -709,70 +743,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the next piece is worked out while this one's first scores are on their way
         Piece nx;
         bool more = walk.next(a, &nx);
-        while (ok && more) {
+        while (more) {
             pc = nx;
-            ok = wait(&ctl.q_full, n & 1, err);
+            ok = ok && wait(&ctl.q_full, n & 1, failed);
             int st = 0, sk = 0;
             bool freed = n == 0;  // the last piece's O has been read
             auto wait_o = [&]() {
-                if (!freed) ok = ok && wait(&ctl.o_free, (n - 1) & 1, err);
+                if (!freed) ok = ok && wait(&ctl.o_free, (n - 1) & 1, failed);
                 freed = true;
             };
             if (pc.two) {
                 int from[2], to[2];
                 pc.range(a, 0, &from[0], &to[0]);
                 pc.range(a, 1, &from[1], &to[1]);
-                if (ok) take(&sk);
+                take(&sk);
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
-                    if (ok && from[s] == 0 && to[s] > 0) issue_s(s, sk, true);
-                if (ok) commit_elected(&ctl.empty[sk]);
-                if (ok && pc.nb == 1) commit_elected(&ctl.q_empty);
+                    if (from[s] == 0 && to[s] > 0) issue_s(s, sk, true);
+                commit_elected(&ctl.empty[sk], ok);
+                if (pc.nb == 1) commit_elected(&ctl.q_empty, ok);
                 more = walk.next(a, &nx);
-                for (int j = 0; j < pc.nb && ok; ++j) {
+                for (int j = 0; j < pc.nb; ++j) {
                     take(&st);
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        if (!ok) break;
                         if (j >= from[s] && j < to[s]) {
                             wait_p(s);
                             wait_o();
-                            if (!ok) break;
                             issue_o(s, st, j == from[s]);
                         }
-                        if (s == 1) commit_elected(&ctl.empty[st]);
+                        if (s == 1) commit_elected(&ctl.empty[st], ok);
                         if (j + 1 < pc.nb) {
                             if (s == 0) take(&sk);
-                            if (!ok) break;
                             if (j + 1 >= from[s] && j + 1 < to[s]) issue_s(s, sk, true);
-                            if (s == 1) commit_elected(&ctl.empty[sk]);
-                            if (s == 1 && j + 2 == pc.nb) commit_elected(&ctl.q_empty);
+                            if (s == 1) commit_elected(&ctl.empty[sk], ok);
+                            if (s == 1 && j + 2 == pc.nb) commit_elected(&ctl.q_empty, ok);
                         }
                     }
                 }
             } else {
-                for (int k = 0; k < 2 && k < pc.nb && ok; ++k) {
+                for (int k = 0; k < 2 && k < pc.nb; ++k) {
                     take(&sk);
-                    if (!ok) break;
                     issue_s(k, sk, false);
-                    commit_elected(&ctl.empty[sk]);
-                    if (k + 1 == pc.nb) commit_elected(&ctl.q_empty);
+                    commit_elected(&ctl.empty[sk], ok);
+                    if (k + 1 == pc.nb) commit_elected(&ctl.q_empty, ok);
                 }
                 more = walk.next(a, &nx);
-                for (int k = 0; k < pc.nb && ok; ++k) {
+                for (int k = 0; k < pc.nb; ++k) {
                     const int s = k & 1;
                     take(&st);
                     wait_p(s);
                     wait_o();
-                    if (!ok) break;
                     issue_o(s, st, k < 2);
-                    commit_elected(&ctl.empty[st]);
+                    commit_elected(&ctl.empty[st], ok);
                     if (k + 2 < pc.nb) {
                         take(&sk);
-                        if (!ok) break;
                         issue_s(s, sk, false);
-                        commit_elected(&ctl.empty[sk]);
-                        if (k + 3 == pc.nb) commit_elected(&ctl.q_empty);
+                        commit_elected(&ctl.empty[sk], ok);
+                        if (k + 3 == pc.nb) commit_elected(&ctl.q_empty, ok);
                     }
                 }
             }
@@ -795,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool notes = pc.notes();
             // the last piece's notes have been read; waited for at every piece, because a parity tells
             // only neighbouring phases apart
-            if (n > 0) ok = wait(&ctl.o_free, (n - 1) & 1, err);
+            if (n > 0) ok = wait(&ctl.o_free, (n - 1) & 1, failed);
             ok = named_bar_and(2, 64, ok);
             int entry = 0;
             uint32_t some = 0;
@@ -807,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kb = pc.kb0 + k;
                 if (!pc.masked(a, kb)) continue;
                 // every masked block is waited for, in order, and the MMA of a block waits for its cleaning
-                ok = named_bar_and(2, 64, wait(&ctl.dirty[nd % kDirty], (nd / kDirty) & 1, err));
+                ok = named_bar_and(2, 64, wait(&ctl.dirty[nd % kDirty], (nd / kDirty) & 1, failed));
                 if (!ok) break;
                 ++nd;
                 uint8_t* blk = smem + S::kOffRing + st * S::kBlock;
@@ -912,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = (pc.kb0 + j) * kKeys;
                 // a row of nobody goes along unmasked: what it computes reaches no other row
                 const bool whole = !valid || (key0 + kKeys - 1 <= pos && key0 >= lo && good == kAll);
-                if (ok && !wait(&ctl.s_full[s], cnt & 1, err)) ok = false;
+                if (ok && !wait(&ctl.s_full[s], cnt & 1, failed)) ok = false;
                 tc_fence_after();
                 if (!busy) {  // no row of this warp is anybody's: its P may stay what it is
                     if (lane == 0) mbar_arrive(&ctl.p_full[s]);
@@ -997,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= corr;
                     if (__any_sync(0xffffffffu, grown) && j > from) {
                         // O of the rows that grew, once the last block's product is in
-                        if (ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, err)) ok = false;
+                        if (ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, failed)) ok = false;
                         tc_fence_after();
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 16) {
@@ -1051,15 +1079,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rounded alike in both sub-tiles' threads
                 l = __fadd_rn(__fmul_rn(l, w0), __fmul_rn(lo2, w1));
             }
-            if (have && ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, err)) ok = false;
-            if (!pc.two && have_o && ok && !wait(&ctl.pv_done[s ^ 1], (cnt_o - 1) & 1, err)) ok = false;
+            if (have && ok && !wait(&ctl.pv_done[s], (cnt - 1) & 1, failed)) ok = false;
+            if (!pc.two && have_o && ok && !wait(&ctl.pv_done[s ^ 1], (cnt_o - 1) & 1, failed)) ok = false;
             // an O that no block went into holds anything
             const bool use = have && w0 != 0.f, use_o = !pc.two && have_o && w1 != 0.f;
             int poisoned = 0;
             if (pc.notes()) {
-                if (ok && !wait(&ctl.clean_done, noted & 1, err)) ok = false;
+                if (ok && !wait(&ctl.clean_done, noted & 1, failed)) ok = false;
                 ++noted;
-                if (ctl.poison.some[0] | ctl.poison.some[1]) poisoned = ctl.poison.n;
+                if (ok && (ctl.poison.some[0] | ctl.poison.some[1])) poisoned = ctl.poison.n;
             }
             tc_fence_after();
             // columns of this thread: its sub-tile's, or half of the joined result's
@@ -1134,6 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == kSoftWarps + 1) {
         tc_fence_after();
+        if (ctl.failed) drain(ctl, kStages);
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
@@ -1367,6 +1396,16 @@ int chunk_split_check(const int32_t* cu, const int32_t* kv_len, int B, int T, in
     return left ? wrong + 1 : wrong;
 }
 
+namespace {
+std::atomic<int> g_test_stall{0};
+}  // namespace
+
+bool chunk_set_test_wait(int kind) {
+    if (kind < 0 || kind >= kStalls) return false;
+    g_test_stall = kind;
+    return true;
+}
+
 cudaError_t chunk_take_error(int* set) {
     cudaError_t e = cudaMemcpyFromSymbol(set, g_chunk_err, sizeof(int));
     const int zero = 0;
@@ -1431,6 +1470,7 @@ dec_status gqa_chunk_attn(const void* q, int64_t ldq, const void* k_pool, const 
     a.v_pool = static_cast<const uint16_t*>(v_pool);
     a.out = static_cast<uint16_t*>(out);
     a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + kJoinBytes);
+    a.stall = g_test_stall;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = d == 128 ? launch<128>(a, q, ldq, k_pool, st) : launch<64>(a, q, ldq, k_pool, st);
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("gqa_chunk_attn: ") + cudaGetErrorString(e));

@@ -161,6 +161,9 @@ bool attn_prefill_tc_ok(const AttnPrefillArgs& a);
 cudaError_t attn_prefill_tc_launch(const AttnPrefillArgs& a, cudaStream_t st, bool pdl);
 // Whether a wait of gqa_chunk_attn's kernel ran out on the current device since the last call (clears it).
 cudaError_t chunk_take_error(int* set);
+// Test hook: in later gqa_chunk_attn launches barriers of one kind (1 .. 10, see attn_chunk.cu) never complete; 0
+// restores normal operation. false: a bad argument.
+bool chunk_set_test_wait(int kind);
 // Host-side check of gqa_chunk_attn's work split (see attn_chunk.cu): violations.
 int chunk_split_check(const int32_t* cu, const int32_t* kv_len, int B, int T, int max_pages, int G, int nkv,
                       int window);

@@ -464,6 +464,12 @@ dec_status dec_test_gemm_wait(int32_t extra_pieces, int64_t limit_cycles);
  * non-positive argument. */
 int32_t dec_test_streamk_check(int32_t M, int32_t N, int32_t K, int32_t ctas);
 
+/* Later gqa_chunk_attn calls wait in vain at barriers of one kind: 1 Q loaded, 2 Q free, 3 a key
+ * or value block loaded, 4 its place free, 5 a value block to be cleaned loaded, 6 scores ready, 7
+ * weights ready, 8 products done, 9 results read, 10 cleaning done; they give up after a second or
+ * two. 0 restores normal operation. */
+dec_status dec_test_chunk_wait(int32_t kind);
+
 /* Host-side check (no GPU needed) of gqa_chunk_attn's work split for given lengths (host arrays
  * here): every (tile, key block) is in one run once, and a tile cut between runs is joined from
  * the run that starts it. Returns the number of violations (0 = sound), or -1 for a bad argument. */

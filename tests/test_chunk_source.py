@@ -10,7 +10,7 @@ SRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), 
 def elected_blocks(src):
     """The bodies of `if (elected()) { .. }`."""
     out = []
-    for m in re.finditer(r"if \(elected\(\)\) \{", src):
+    for m in re.finditer(r"if \(elected\(\)( && ok)?\) \{", src):
         depth, at = 1, m.end()
         while depth:
             depth += {"{": 1, "}": -1}.get(src[at], 0)
@@ -30,4 +30,4 @@ def test_products_and_commits_are_the_elected_lanes():
     # a commit in assembly of its own elects its lane
     for asm in re.findall(r"asm volatile\((.*?)\);", src, re.S):
         if "tcgen05.commit" in asm:
-            assert "elect.sync" in asm and "@e tcgen05.commit" in asm
+            assert "elect.sync _|e" in asm and "@e tcgen05.commit" in asm

@@ -48,3 +48,33 @@ def test_verify_temperatures_and_counts_written_just_before_the_call():
         torch.cuda.synchronize()
         for g, w in zip(got, want):
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+# ------------------------------------------------------------------ gqa_chunk_attn
+
+@pytest.mark.parametrize("d,kind", [(128, k) for k in range(1, 11)] + [(64, k) for k in (1, 4, 5, 7)])
+def test_chunk_wait_that_runs_out_is_reported_and_the_next_call_is_correct(d, kind):
+    """Whichever barrier never completes, with loads and products in flight: the call ends with an
+    error status, and the next one finds shared memory and TMEM in order."""
+    # eight tiles of six blocks a CTA, the last of each cleaned; some tiles of two sub-tiles
+    rows = [(2, 700)] * 590 + [(100, 700)] * 5
+    inp = chunk_inputs(rows, 8, 2, d, 61)
+    q, kp, vp, table, cu, lens = inp
+    args = (q, kp, vp, ints(table), ints(cu), ints(lens), d ** -0.5)
+    want, got = torch.zeros_like(q), torch.zeros_like(q)
+    dec.gqa_chunk_attn(*args, want)
+    dec.check_standalone()
+    dec.test_chunk_wait(kind)
+    try:
+        dec.gqa_chunk_attn(*args, got)
+        with pytest.raises(dec.DecError) as e:
+            dec.check_standalone()
+        assert e.value.status == "TIMEOUT"
+    finally:
+        dec.test_chunk_wait(0)
+    dec.check_standalone()  # the word was cleared
+    for _ in range(2):
+        got.zero_()
+        dec.gqa_chunk_attn(*args, got)
+        dec.check_standalone()
+        assert torch.equal(got, want)

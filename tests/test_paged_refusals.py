@@ -168,3 +168,9 @@ def test_wrappers_name_a_missing_tensor():
             for wrong in (None, [1, 2]):
                 with pytest.raises(TypeError, match="expected a torch tensor"):
                     call(*args[:k], wrong, *args[k + 1:])
+
+
+def test_wait_hook_takes_known_barriers_only():
+    L = dec.lib()
+    assert L.dec_test_chunk_wait(-1) == BAD and L.dec_test_chunk_wait(11) == BAD
+    assert L.dec_test_chunk_wait(0) == 0
