@@ -70,8 +70,12 @@ DEC_DEVINL int drafts_of(const VerifyArgs& a, int b) {
     return a.count ? min(max(a.count[b], 0), a.n) : a.n;
 }
 
-// log2(e) / T; a temperature so small that it overflows is a temperature of 1e-30
-DEC_DEVINL float log2e_over(float T) { return T > 0.f ? fminf(1.4426950408889634f / T, 1e30f) : 0.f; }
+// log2(e) / T for T > 0, as fp32 and as fp64. A temperature below 2^-126, the smallest normal number, counts as that (so
+// this stays finite). At T = +inf every token has the same weight but those of -inf: the factor is the
+// smallest number above 0, since -inf times 0 would be NaN.
+constexpr float kMinT = 0x1p-126f;
+DEC_DEVINL float log2e_over(float T) { return fmaxf(1.4426950408889634f / fmaxf(T, kMinT), 0x1p-149f); }
+DEC_DEVINL double log2e_over_d(float T) { return fmax(1.4426950408889634074 / (double)fmaxf(T, kMinT), 1e-300); }
 
 DEC_DEVINL float ex2f(float x) {
     float y;
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
     const int nb = drafts_of(a, b);
     const float T = a.temp ? a.temp[b] : 1.f;
     const bool warm = T > 0.f;
-    const double c = warm ? 1.4426950408889634074 / (double)T : 0.0;  // e^(l / T) = 2^(c l)
+    const double c = log2e_over_d(T);  // e^(l / T) = 2^(c l)
     const float k = log2e_over(T);
 
     // ---- the rows' statistics from their pieces, a warp a row

@@ -425,7 +425,8 @@ int64_t gqa_chunk_attn_workspace(int32_t d);
  *           draft (or NULL) likewise, n rows a sequence. -inf is a token of no probability; +inf
  *           and NaN are not allowed (no out-of-range access follows, but the tokens mean nothing)
  *   draft_tok device int32 [B][n]; n_draft device int32 [B], taken into [0, n], or NULL: n
- *   temperature device fp32 [B] or NULL: 1; u_accept device fp32 [B][n], u_sample device fp32 [B],
+ *   temperature device fp32 [B] or NULL: 1 (+inf: all tokens but those of -inf are equally likely; a
+ *           positive one below 2^-126 counts as 2^-126); u_accept device fp32 [B][n], u_sample device fp32 [B],
  *           in [0, 1)
  *   n_accepted device int32 [B], out; tokens device int32 [B][n + 1], out: the accepted drafts, the
  *           next token (-1 when every logit is -inf), then -1

@@ -50,6 +50,43 @@ def test_verify_temperatures_and_counts_written_just_before_the_call():
             assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+@pytest.mark.parametrize("draft", [0, 1])
+def test_verify_at_infinite_temperature(draft):
+    """Every token that is not masked is as likely as any other."""
+    x = verify_inputs(12, 4, 3000, draft, 52)
+    x["temp"][:9] = math.inf
+    if not draft:
+        x["u"][:, :2] /= 3000  # about 1 / V: some of these drafts are accepted
+    acc = check_verify(x)
+    assert (acc[:9] == 4).all() if draft else 0 < acc[:9].sum() < 36
+    # with masked tokens: as logits of 0 at temperature 1
+    x["target"][:, :, 100:2500] = -math.inf
+    flat = dict(x, target=torch.where(torch.isinf(x["target"]), -math.inf, 0.0), temp=np.ones(12, np.float32))
+    if draft:
+        x["draft"][:, :, 2000:] = -math.inf
+        flat["draft"] = torch.where(torch.isinf(x["draft"]), -math.inf, 0.0)
+    x["temp"][:] = math.inf
+    x["tok"][:] = np.random.default_rng(52).integers(0, 3000, (12, 4))
+    check_verify(flat)
+    for got, want in zip(run_verify(x), run_verify(flat)):
+        assert np.array_equal(got, want)
+
+
+def test_verify_temperatures_far_from_one():
+    """The distribution depends on logits over temperature, at any scale of the two."""
+    x = verify_inputs(40, 3, 2000, 1, 53)
+    scale = np.float32(2.0) ** np.repeat([-116, -60, 60, 116], 10).astype(np.float32)
+    for k in ("target", "draft"):
+        x[k] = x[k] * torch.tensor(scale, device="cuda")[:, None, None]
+    x["temp"] = x["temp"] * scale
+    acc = check_verify(x)
+    assert 0 < acc.sum() < 120
+    # one token has everything; nearly equal chances
+    x = verify_inputs(8, 3, 2000, 1, 54)
+    x["temp"][:] = [1e-30, 1e-38, 1e-45, 1e-10, 1e10, 1e30, 3e38, 1e5]
+    check_verify(x)
+
+
 # ------------------------------------------------------------------ gqa_chunk_attn
 
 @pytest.mark.parametrize("d,kind", [(128, k) for k in range(1, 11)] + [(64, k) for k in (1, 4, 5, 7)])
