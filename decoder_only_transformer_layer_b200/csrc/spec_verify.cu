@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
         const Stat p = sh.row[i];
         int v = 0;
         if (!warm) {
-            v = x == p.arg;
+            v = x == p.arg && x < a.V;  // the argmax of a row of -inf is none
         } else if (x >= 0 && x < a.V) {
             // u q < p, multiplied out
             const double u = a.u[(size_t)b * a.n + i];

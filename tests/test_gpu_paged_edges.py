@@ -87,6 +87,18 @@ def test_verify_temperatures_far_from_one():
     check_verify(x)
 
 
+def test_verify_greedy_rows_without_a_token_accept_nothing():
+    x = verify_inputs(6, 3, 3000, 0, 55)
+    x["temp"][:5] = [0.0, -1.0, 0.0, 0.0, 0.0]
+    x["target"][:4, 1] = -math.inf
+    x["target"][4] = -math.inf
+    best = x["target"].argmax(-1).cpu().numpy()
+    x["tok"][:] = best[:, :3]
+    x["tok"][:5, 1] = [2 ** 31 - 1, 2 ** 31 - 1, 0, -1, 2 ** 31 - 1]
+    x["tok"][4, 0] = 2 ** 31 - 1
+    assert list(check_verify(x)[:5]) == [1, 1, 1, 1, 0]
+
+
 # ------------------------------------------------------------------ gqa_chunk_attn
 
 @pytest.mark.parametrize("d,kind", [(128, k) for k in range(1, 11)] + [(64, k) for k in (1, 4, 5, 7)])
