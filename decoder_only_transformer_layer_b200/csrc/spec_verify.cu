@@ -14,7 +14,7 @@
 // reads again (from L2). A drawn token lies between two neighbouring values of a
 // cumulative sum over the whole vocabulary, a spacing of 1e-5 or less, so that row's
 // exponentials, sums and cumulative sums are in fp64. An acceptance whose two sides are
-// too close for the fp32 sums is decided again with fp64 sums.
+// too close for the fp32 sums (verify_margin) is decided again with fp64 sums.
 //
 // Measured (B200): 32 sequences of up to 7 drafts over 128256 tokens, 158 MB of rows that count, take 61 us
 // on the device: 27 for the first kernel (5.8 TB/s) and 34 for the draw. For a rejected row that is two passes
@@ -59,6 +59,7 @@ struct VerifyArgs {
     const float* u;          // [B][n]
     const float* us;         // [B]
     int B, n, V, splits, piece;
+    double margin;           // sides of an acceptance closer than this (relative) are compared again in fp64
     Stat* stats;             // [B][2n + 1][splits]: target rows, then draft rows
     int32_t* accepted;
     int32_t* tokens;         // [B][n + 1]
@@ -334,9 +335,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) verify_pick_kernel(VerifyArgs
                 right *= (double)q.s;
             }
             v = left < right;
-            // the fp32 sums are within 1e-5 of the exact ones: a term is off by 2^-22 and by 2^-23 of its exponent,
-            // which is below 40 where the term counts
-            if (fabs(left - right) <= 4e-5 * fmax(left, right)) v = 2;
+            if (fabs(left - right) <= a.margin * fmax(left, right)) v = 2;
         }
         sh.verdict[i] = v;
     }
@@ -525,6 +524,18 @@ int verify_splits(int B, int n, int V) {
     return s;
 }
 
+// How far apart (relative) the two sides of an acceptance have to be for the fp32 sums to decide it. In units of
+// 2^-24, a term of a sum is off by 4 for each ex2 and 1 for each product or addition on its way: its own ex2; 12
+// for each step over 16 values a thread takes (one move of the maximum, six additions) and for the row's ends; 6
+// for each join (5 and 7 in a CTA, one for every 32 pieces and 5 over the pieces). All exponents on that way add up to the
+// term's own, off by 4 x 2^-24 of itself; it is below 60 where the term counts (2^30 terms of 2^-60 are
+// 2^-30), so 4 x 60 x ln 2 = 166 more. Two sums, and a quarter more for what the errors' products add. For a
+// vocabulary of 128256 that is 4.7e-5 (pieces of 4008) to 1e-4 (one piece): one acceptance in 10^4 costs fp64 sums.
+double verify_margin(int piece, int splits) {
+    const double steps = piece / (4.0 * kBatch * kStatThreads) + 2.0, joins = 17.0 + (splits + 31) / 32;
+    return 2.5 * (170.0 + 12.0 * steps + 6.0 * joins) * 0x1p-24;
+}
+
 }  // namespace
 }  // namespace dec
 
@@ -570,6 +581,7 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     a.V = V;
     a.splits = verify_splits(B, n, V);
     a.piece = (V + a.splits - 1) / a.splits;
+    a.margin = verify_margin(a.piece, a.splits);
     a.stats = static_cast<Stat*>(workspace);
     a.accepted = n_accepted;
     a.tokens = tokens;

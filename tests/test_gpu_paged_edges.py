@@ -99,6 +99,30 @@ def test_verify_greedy_rows_without_a_token_accept_nothing():
     assert list(check_verify(x)[:5]) == [1, 1, 1, 1, 0]
 
 
+def test_verify_close_calls_of_long_rows():
+    """Acceptances next to equality where a thread sums 65536 values in fp32: equal logits, at which every
+    step rounds the same way. 37 sequences of 64 places put a row into one piece."""
+    B, n, V = 37, 64, 1 << 24
+    t = torch.empty((1, n + 1, V), device="cuda")  # the counts see to it that only two rows are used
+    t[:, 0] = -0.714
+    t[:, 0, :4096] = 0.0  # every thread's first largest value
+    t[:, 0, 9000] = 14.0
+    t[:, 1] = 0.0
+    t[:, 1, 7] = 40.0  # the token after an accepted draft
+    w = math.exp(float(np.float32(-0.714)))
+    p = math.exp(14.0) / (math.exp(14.0) + 4096 + (V - 4097) * w)
+    u = np.zeros((B, n), np.float32)
+    u[:, 0] = (p * (1 + (np.arange(B) - 18.5) * 1e-5)).astype(np.float32)
+    acc, tokens = torch.zeros(B, **I32), torch.zeros((B, n + 1), **I32)
+    dec.spec_verify(t.expand(B, n + 1, V), None, ints(np.full((B, n), 9000)), torch.ones(B, **I32), None,
+                    torch.tensor(u).cuda(), torch.full((B,), 0.5, device="cuda"), acc, tokens)
+    # the nearest uniform is 5e-6 of p away, many steps of its type
+    want = (u[:, 0].astype(np.float64) < p).astype(int)
+    assert 0 < want.sum() < B and np.array_equal(acc.cpu().numpy(), want)
+    tokens = tokens.cpu().numpy()
+    assert (tokens[want == 1, 0] == 9000).all() and (tokens[want == 1, 1] == 7).all()
+
+
 # ------------------------------------------------------------------ gqa_chunk_attn
 
 @pytest.mark.parametrize("d,kind", [(128, k) for k in range(1, 11)] + [(64, k) for k in (1, 4, 5, 7)])
