@@ -26,6 +26,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <exception>
 #include <mutex>
 #include <set>
@@ -516,11 +517,14 @@ cudaError_t allow_wide_cluster() {
     return e;
 }
 
+// Pieces of a row: of at most 4096 values, or longer where pieces that short would be more than fill the GPU
+// several times over.
+constexpr int kPiece = 4096, kPieces = 148 * 32;
+
 int verify_splits(int B, int n, int V) {
-    // pieces of at least 4096 values, and enough of them to fill the GPU several times over
     const long long rows = (long long)B * (2 * n + 1);
-    int s = (V + 4095) / 4096;
-    while (s > 1 && rows * s > 148 * 32) s = (s + 1) / 2;
+    int s = (V + kPiece - 1) / kPiece;
+    while (s > 1 && rows * s > kPieces) s = (s + 1) / 2;
     return s;
 }
 
@@ -545,7 +549,9 @@ extern "C" {
 
 int64_t spec_verify_workspace(int32_t B, int32_t n, int32_t V) {
     if (B <= 0 || n < 0 || V <= 0) return 0;
-    return (int64_t)B * (2 * (int64_t)n + 1) * verify_splits(B, n, V) * (int64_t)sizeof(Stat);
+    // no fewer than verify_splits gives, and never fewer for more sequences, drafts or values
+    const int64_t rows = (int64_t)B * (2 * (int64_t)n + 1), most = std::max<int64_t>(kPieces, rows);
+    return std::min(rows * ((V - 1) / kPiece + 1), most) * (int64_t)sizeof(Stat);
 }
 
 dec_status spec_verify(const float* target, int64_t target_row, int64_t target_seq, const float* draft,

@@ -430,7 +430,8 @@ int64_t gqa_chunk_attn_workspace(int32_t d);
  *           in [0, 1)
  *   n_accepted device int32 [B], out; tokens device int32 [B][n + 1], out: the accepted drafts, the
  *           next token (-1 when every logit is -inf), then -1
- *   workspace device scratch of spec_verify_workspace(B, n, V) bytes, 16-byte aligned
+ *   workspace device scratch of spec_verify_workspace(B, n, V) bytes (one for the largest B, n and V serves
+ *           smaller ones too), 16-byte aligned
  * A sequence that held L cache rows and forwarded its last token and n_b drafts goes on with
  * L + n_accepted + 1 rows (paged_resize or dec_truncate).
  * Errors: NULL pointer, a bad size or stride -> INVALID_ARG; n > 64, B (2n + 1) > 65535 ->

@@ -174,3 +174,28 @@ def test_wait_hook_takes_known_barriers_only():
     L = dec.lib()
     assert L.dec_test_chunk_wait(-1) == BAD and L.dec_test_chunk_wait(11) == BAD
     assert L.dec_test_chunk_wait(0) == 0
+
+
+def test_a_workspace_for_the_largest_call_serves_smaller_ones():
+    size = dec.lib().spec_verify_workspace
+    Bs, ns, Vs = [*range(1, 80), 147, 148, 149, 300, 500], [*range(0, 10), 31, 63, 64], [1, 500, 4096, 4097, 8192, 32003,
+                                                                                        49152, 128256, 151936, 1 << 20]
+    for n in ns:
+        for V in Vs:
+            sizes = [size(B, n, V) for B in Bs]
+            assert sizes == sorted(sizes) and sizes[0] > 0
+    for B in Bs:
+        for V in Vs:
+            sizes = [size(B, n, V) for n in ns]
+            assert sizes == sorted(sizes)
+        for n in ns:
+            sizes = [size(B, n, V) for V in Vs]
+            assert sizes == sorted(sizes)
+    # and each serves the call itself: one piece a row at least, the pieces the launch takes at most
+    for B in Bs:
+        for n in ns:
+            for V in Vs:
+                rows, s = B * (2 * n + 1), -(-V // 4096)
+                while s > 1 and rows * s > 148 * 32:
+                    s = (s + 1) // 2
+                assert size(B, n, V) >= 16 * rows * s
