@@ -1541,21 +1541,25 @@ dec_status dec_check_standalone(dec_stream_t stream) {
     CUDA_TRY(cudaStreamSynchronize(st));
     int chunk = 0;
     CUDA_TRY(chunk_take_error(&chunk));
-    if (chunk) return fail(DEC_ERR_TIMEOUT, "a bounded device wait of gqa_chunk_attn ran out; its output is not valid");
     std::lock_guard<std::mutex> lock(g_scratch_mu);
     int dev = 0;
     cudaGetDevice(&dev);
     auto it = g_scratch.find(dev);
-    if (it == g_scratch.end() || !it->second.err) return DEC_OK;
-    Scratch& S = it->second;
     int e = 0;
-    CUDA_TRY(cudaMemcpy(&e, S.err, sizeof(int), cudaMemcpyDeviceToHost));
-    if (!e) return DEC_OK;
-    // clear the word and the GEMM tile counters an abandoned reduction can leave behind
-    CUDA_TRY(cudaMemset(S.err, 0, sizeof(int)));
-    if (S.cnt) CUDA_TRY(cudaMemset(S.cnt, 0, sizeof(int) * S.cnt_n));
-    CUDA_TRY(cudaDeviceSynchronize());
-    return fail(DEC_ERR_TIMEOUT, "a bounded device wait of a standalone call ran out; its output is not valid");
+    if (it != g_scratch.end() && it->second.err) {
+        Scratch& S = it->second;
+        CUDA_TRY(cudaMemcpy(&e, S.err, sizeof(int), cudaMemcpyDeviceToHost));
+        if (e) {
+            // clear the word and the GEMM tile counters an abandoned reduction can leave behind
+            CUDA_TRY(cudaMemset(S.err, 0, sizeof(int)));
+            if (S.cnt) CUDA_TRY(cudaMemset(S.cnt, 0, sizeof(int) * S.cnt_n));
+            CUDA_TRY(cudaDeviceSynchronize());
+        }
+    }
+    if (!e && !chunk) return DEC_OK;
+    const char* who = e && chunk ? "gqa_chunk_attn and one of another standalone call"
+                      : e        ? "a standalone call" : "gqa_chunk_attn";
+    return fail(DEC_ERR_TIMEOUT, std::string("a bounded device wait of ") + who + " ran out; its output is not valid");
 }
 
 dec_status dec_test_fail_alloc(int32_t n) {

@@ -151,3 +151,35 @@ def test_chunk_wait_that_runs_out_is_reported_and_the_next_call_is_correct(d, ki
         dec.gqa_chunk_attn(*args, got)
         dec.check_standalone()
         assert torch.equal(got, want)
+
+
+def test_a_check_reports_and_clears_every_kind_of_time_out():
+    """A wait of gqa_chunk_attn and one of the tensor-core GEMM run out: one check tells, and the next
+    call of either is correct."""
+    from _util import to_dev_bf16
+    from test_gpu_boundary import _gemm_case
+    W, x, _ = _gemm_case()
+    Wd, xd = to_dev_bf16(W, torch), to_dev_bf16(x, torch)
+    y, good = (torch.zeros((x.shape[0], W.shape[0]), device="cuda") for _ in range(2))
+    q, kp, vp, table, cu, lens = chunk_inputs([(2, 300)] * 40, 8, 2, 64, 63)
+    args = (q, kp, vp, ints(table), ints(cu), ints(lens), 0.125)
+    want, got = torch.zeros_like(q), torch.zeros_like(q)
+    dec.weight_gemv(Wd, xd, good)
+    dec.gqa_chunk_attn(*args, want)
+    dec.check_standalone()
+    dec.test_gemm_wait(1, 1 << 21)
+    dec.test_chunk_wait(7)
+    try:
+        dec.weight_gemv(Wd, xd, y)
+        dec.gqa_chunk_attn(*args, got)
+        with pytest.raises(dec.DecError) as e:
+            dec.check_standalone()
+        assert e.value.status == "TIMEOUT"
+    finally:
+        dec.test_gemm_wait(0, 0)
+        dec.test_chunk_wait(0)
+    dec.check_standalone()  # nothing is left of either
+    dec.weight_gemv(Wd, xd, y)
+    dec.gqa_chunk_attn(*args, got)
+    dec.check_standalone()
+    assert torch.equal(y, good) and torch.equal(got, want)
