@@ -1406,11 +1406,26 @@ bool chunk_set_test_wait(int kind) {
     return true;
 }
 
-cudaError_t chunk_take_error(int* set) {
-    cudaError_t e = cudaMemcpyFromSymbol(set, g_chunk_err, sizeof(int));
+namespace {
+// Devices on which gqa_chunk_attn has been called (index 63: that one and all above).
+std::atomic<bool> g_used[64];
+
+std::atomic<bool>& used_here() {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    return g_used[dev < 63 ? dev : 63];
+}
+}  // namespace
+
+cudaError_t chunk_take_error(int* set, cudaStream_t st) {
+    *set = 0;
+    if (!used_here()) return cudaSuccess;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(set, g_chunk_err, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess || !*set) return e;
     const int zero = 0;
-    if (e == cudaSuccess && *set) e = cudaMemcpyToSymbol(g_chunk_err, &zero, sizeof(int));
-    return e;
+    e = cudaMemcpyToSymbolAsync(g_chunk_err, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 
 }  // namespace dec
@@ -1472,6 +1487,7 @@ dec_status gqa_chunk_attn(const void* q, int64_t ldq, const void* k_pool, const 
     a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + kJoinBytes);
     a.stall = g_test_stall;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    used_here() = true;
     cudaError_t e = d == 128 ? launch<128>(a, q, ldq, k_pool, st) : launch<64>(a, q, ldq, k_pool, st);
     if (e != cudaSuccess) return bad(DEC_ERR_CUDA, std::string("gqa_chunk_attn: ") + cudaGetErrorString(e));
     return DEC_OK;

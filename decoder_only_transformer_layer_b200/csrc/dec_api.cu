@@ -1540,7 +1540,7 @@ dec_status dec_check_standalone(dec_stream_t stream) {
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     CUDA_TRY(cudaStreamSynchronize(st));
     int chunk = 0;
-    CUDA_TRY(chunk_take_error(&chunk));
+    CUDA_TRY(chunk_take_error(&chunk, st));
     std::lock_guard<std::mutex> lock(g_scratch_mu);
     int dev = 0;
     cudaGetDevice(&dev);

@@ -159,8 +159,9 @@ cudaError_t attn_prefill_launch(const AttnPrefillArgs& a, cudaStream_t st, bool 
 // The tensor-core prefill attention (tcgen05, TMEM): head dim 128, power-of-two groups.
 bool attn_prefill_tc_ok(const AttnPrefillArgs& a);
 cudaError_t attn_prefill_tc_launch(const AttnPrefillArgs& a, cudaStream_t st, bool pdl);
-// Whether a wait of gqa_chunk_attn's kernel ran out on the current device since the last call (clears it).
-cudaError_t chunk_take_error(int* set);
+// Whether a wait of gqa_chunk_attn's kernel ran out on the current device since the last call (clears it). Copies on
+// `st` and waits for it, but only where gqa_chunk_attn has been called.
+cudaError_t chunk_take_error(int* set, cudaStream_t st);
 // Test hook: in later gqa_chunk_attn launches barriers of one kind (1 .. 10, see attn_chunk.cu) never complete; 0
 // restores normal operation. false: a bad argument.
 bool chunk_set_test_wait(int kind);

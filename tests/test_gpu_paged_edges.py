@@ -183,3 +183,42 @@ def test_a_check_reports_and_clears_every_kind_of_time_out():
     dec.gqa_chunk_attn(*args, got)
     dec.check_standalone()
     assert torch.equal(y, good) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("used", [False, True])
+def test_a_check_of_one_stream_does_not_wait_for_others(used):
+    """Nothing goes through the default stream, which would wait for every stream that is not marked
+    as independent of it (here one that sleeps for about two seconds)."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import ctypes, time
+import torch
+import decoder_only_transformer_layer_b200 as dec
+bf = lambda *s: torch.ones(s, dtype=torch.bfloat16, device="cuda")
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+q, k, v, out = bf(3, 8, 64), bf(2, 2, 16, 64), bf(2, 2, 16, 64), bf(3, 8, 64) * 0
+args = (q, k, v, i(0, 1).view(1, 2), i(0, 3), i(3), 0.125, out)
+side = torch.cuda.Stream()
+handle = ctypes.c_uint64(0)
+assert torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(handle)) == 0
+slow = torch.cuda.ExternalStream(handle.value)
+for sleep in (1000, 1 << 32):
+    torch.cuda.synchronize()
+    with torch.cuda.stream(slow):
+        torch.cuda._sleep(sleep)
+    with torch.cuda.stream(side):
+        if {used}:
+            dec.gqa_chunk_attn(*args)
+        t0 = time.monotonic()
+        dec.check_standalone()
+        waited = time.monotonic() - t0
+    assert sleep == 1000 or not slow.query()
+    torch.cuda.synchronize()
+assert waited < 0.5, waited
+print("ok")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
