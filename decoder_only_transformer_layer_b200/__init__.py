@@ -527,8 +527,8 @@ def gqa_chunk_attn(q, k_pool, v_pool, block_table, cu_rows, kv_len, scale, out, 
 def spec_verify(target, draft, draft_tok, n_draft, temperature, u_accept, u_sample, n_accepted, tokens,
                 workspace=None, stream=None):
     """Keep or reject drafted tokens against the target's distribution. Device tensors: target fp32
-    [B][n + 1][V] logits, draft fp32 [B][n][V] logits or None (each draft certain), both with
-    rows and sequences at any stride; draft_tok int32 [B][n]; n_draft int32 [B] or None (all n);
+    [B][n + 1][V] logits, draft fp32 [B][n][V] logits or None (each draft certain), rows at least V
+    apart and sequences at any stride; draft_tok int32 [B][n]; n_draft int32 [B] or None (all n);
     temperature fp32 [B] or None (1; <= 0 is greedy); u_accept fp32 [B][n] and u_sample fp32 [B] in
     [0, 1); out: n_accepted int32 [B], tokens int32 [B][n + 1] (accepted drafts, the next token,
     -1). workspace as in gqa_chunk_attn (spec_verify_workspace(B, n, V) bytes)."""

@@ -359,7 +359,7 @@ dec_status weight_gemv_q8(const void* Wq, const float* scale, const void* x, int
  *               outside [0, n_pages)), else DEC_ERR_CONTEXT_OVERFLOW (a length above
  *               16 * max_pages), else DEC_ERR_PAGES_EXHAUSTED (A > F)
  * Errors on the host: NULL pointer or a bad size -> INVALID_ARG; B > 4096, T > 2^30, n_pages or
- * max_pages above 2^27, page_size other than 16 -> UNSUPPORTED. */
+ * max_pages not below 2^27, page_size other than 16 -> UNSUPPORTED. */
 dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t B, int32_t* block_table,
                         int32_t max_pages, int32_t page_size, int32_t* free_pages, int32_t n_pages, int32_t* n_free,
                         int32_t* cu_rows, int32_t* slot, int32_t* row_pos, int32_t T, int32_t* status,
@@ -375,9 +375,10 @@ dec_status paged_resize(const int32_t* old_len, const int32_t* new_len, int32_t 
  *   row_pos device int32 [T]: position of the row (half-split pairs, angle
  *           p * rope_base^(-2i/d), evaluated in fp64)
  *   q_out   device bf16 [T][nq][d]; k_pool/v_pool device bf16 [n_pages][nkv][16][d]
- * d must be 64 or 128, page_size 16. Errors: NULL pointer, a bad size or ld below
- * (nq + 2 nkv) d -> INVALID_ARG; another d or page_size, or q_out, a pool or a gain off the
- * 16-byte grid (qkv may lie anywhere) -> UNSUPPORTED. T = 0 does nothing. */
+ * d must be 64 or 128, page_size 16. Errors: NULL pointer, a bad size, ld below (nq + 2 nkv) d, a
+ * rope_base not above 0 or, with a gain, a negative eps -> INVALID_ARG; another d or page_size,
+ * T > 2^30, n_pages >= 2^27, nq or nkv > 2^20, or q_out, a pool or a gain off the 16-byte grid
+ * (qkv may lie anywhere) -> UNSUPPORTED. T = 0 does nothing. */
 dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, const float* k_norm, float eps,
                              float rope_base, const int32_t* slot, const int32_t* row_pos, int32_t T, int32_t nq,
                              int32_t nkv, int32_t d, int32_t page_size, void* q_out, void* k_pool, void* v_pool,
@@ -399,11 +400,13 @@ dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, 
  * -inf. A cache row whose table entry lies outside [0, n_pages) is not attended. Keys a row
  * does not attend never reach it, whatever the pool holds there (NaN and infinities included).
  * kv_len above 16 * max_pages counts as 16 * max_pages.
- * Errors: NULL pointer, a bad size, scale not positive or ldq below nq*d -> INVALID_ARG; more
- * than 16 query heads a kv head, d other than 64 / 128, page_size other than 16, B > 4096, scale
- * outside 2^-40 .. 2^40, a softcap above 0 and below 2^-20, or an address or stride off the 16-byte
- * grid -> UNSUPPORTED. T = 0 does nothing. Scores, q . K * scale, have to fit fp32: a row with one
- * that is NaN or +inf is NaN. A device wait that runs out is reported by dec_check_standalone. */
+ * Errors: NULL pointer, a bad size, scale not positive, a negative window or softcap, ldq below nq*d
+ * or a workspace too small -> INVALID_ARG; more than 16 query heads a kv head, d other than 64 / 128,
+ * page_size other than 16, B > 4096, T > 2^30, max_pages > 2^26, n_pages * nkv >= 2^27, scale outside
+ * 2^-40 .. 2^40, a softcap above 0 and below 2^-20, or an address or stride off the 16-byte grid ->
+ * UNSUPPORTED. T = 0 does nothing. Scores, q . K * scale, have to fit fp32: a row with one that is NaN,
+ * or +inf where there is no softcap (under one it counts as softcap), is NaN. A device wait that runs
+ * out is reported by dec_check_standalone. */
 dec_status gqa_chunk_attn(const void* q, int64_t ldq, const void* k_pool, const void* v_pool, int32_t n_pages,
                           const int32_t* block_table, int32_t max_pages, const int32_t* cu_rows,
                           const int32_t* kv_len, int32_t B, int32_t T, int32_t nq, int32_t nkv, int32_t d,
@@ -434,7 +437,8 @@ int64_t gqa_chunk_attn_workspace(int32_t d);
  *           smaller ones too), 16-byte aligned
  * A sequence that held L cache rows and forwarded its last token and n_b drafts goes on with
  * L + n_accepted + 1 rows (paged_resize or dec_truncate).
- * Errors: NULL pointer, a bad size or stride -> INVALID_ARG; n > 64, B (2n + 1) > 65535 ->
+ * Errors: NULL pointer, a bad size, a row stride below V, a negative stride or a workspace too small or
+ * off the 16-byte grid -> INVALID_ARG; n > 64, B (2n + 1) > 65535, V > 2^30 ->
  * UNSUPPORTED. */
 dec_status spec_verify(const float* target, int64_t target_row, int64_t target_seq, const float* draft,
                        int64_t draft_row, int64_t draft_seq, const int32_t* draft_tok, const int32_t* n_draft,

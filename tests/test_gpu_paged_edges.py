@@ -5,9 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-import _paged_plain as plain
 import decoder_only_transformer_layer_b200 as dec
-from test_gpu_paged_step import I32, check_chunk, check_verify, chunk_inputs, f64, ints, verify_inputs
+from test_gpu_paged_step import I32, check_chunk, check_verify, chunk_inputs, ints, verify_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -123,6 +122,14 @@ def test_verify_close_calls_of_long_rows():
     assert (tokens[want == 1, 0] == 9000).all() and (tokens[want == 1, 1] == 7).all()
 
 
+@pytest.mark.parametrize("B,n,V", [(9, 3, 3000), (10, 3, 3000), (16, 2, 3000), (17, 2, 3000), (18, 2, 5000), (19, 2, 3000),
+                                   (36, 2, 3000), (37, 2, 3000), (73, 2, 1500), (74, 2, 1500), (75, 2, 1500),
+                                   (147, 1, 1000), (148, 1, 1000), (149, 1, 1000), (300, 1, 1000), (100, 7, 20000),
+                                   (40, 30, 4097)])
+def test_verify_batches_around_the_ways_of_sharing_the_work(B, n, V):
+    check_verify(verify_inputs(B, n, V, 1, B + n))
+
+
 # ------------------------------------------------------------------ gqa_chunk_attn
 
 @pytest.mark.parametrize("d,kind", [(128, k) for k in range(1, 11)] + [(64, k) for k in (1, 4, 5, 7)])
@@ -151,6 +158,18 @@ def test_chunk_wait_that_runs_out_is_reported_and_the_next_call_is_correct(d, ki
         dec.gqa_chunk_attn(*args, got)
         dec.check_standalone()
         assert torch.equal(got, want)
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("val", [math.inf, -math.inf])
+def test_chunk_scores_that_are_not_finite(val, cap):
+    """A score of -inf leaves its key out, one of +inf makes its row NaN; under a cap both are the cap."""
+    inp = chunk_inputs([(200, 330), (3, 40), (1, 600), (2, 700)], 8, 2, 128, 62)
+    table = inp[3]
+    for b, j in ((0, 250), (0, 20), (1, 39), (2, 300), (3, 699)):
+        inp[1][table[b, j // 16], :, j % 16, 5] = val
+    out = check_chunk(inp, cap=cap)
+    assert torch.isnan(out).any() == (cap == 0.0)
+
 
 
 def test_a_check_reports_and_clears_every_kind_of_time_out():
