@@ -195,7 +195,7 @@ DEC_DEVINL void exp2_d(double (&x)[N], const double* table) {
     bool in[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        // -1000 and above, by the upper word (0xC08F4000 is -1000's); NaN counts as below
+        // -1000 and above, by the upper word (0xC08F4000 is -1000's; a NaN may give anything)
         in[i] = (unsigned)__double2hiint(x[i]) < 0xC08F4000u;
         const double t = x[i] + kMagic;
         n[i] = __double2loint(t);
@@ -603,11 +603,16 @@ dec_status spec_verify(const float* target, int64_t target_row, int64_t target_s
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stats_kernel, a);
     if (e == cudaSuccess) e = allow_wide_cluster();
-    // as many CTAs a sequence as can all be on the SMs, two each: with few sequences the draw is shorter the
-    // more SMs it has; with many, greedy sequences end at once and leave their SMs to the others (32 sequences,
-    // half of them greedy: 8 CTAs each 60.6 us for the call, 16 each 60.8, and 4 each 2 us more than 8)
-    int C = kPickCluster;
-    while (C > 1 && (int64_t)B * C > 2 * 148) C /= 2;
+    // CTAs a sequence: the draw is shorter the more SMs it has, while all its clusters run at once or nearly so. The SMs
+    // have 296 places, but a cluster's lie in one GPC: 14 clusters of 16 run at once, 33 of 8, 71 of 4, 148 of 2.
+    // So 16 up to 18 sequences, 8 up to 52, 4 up to 105, else 2. Device time of a call in us, n drafts, thousands of tokens:
+    //   16 / 8: n 4, 128k   8 sequences 27.5 / 32.5, 16 42.3 / 42.1, 18 44.1 / 46.1, 20 47.5 / 50.1, 24 52.9 / 50.3,
+    //           32 69.2 / 58.3;  49k, 20: n 1 23.6 / 20.1, n 4 34.3 / 27.3
+    //   8 / 4:  n 4, 128k   37 69.3 / 82.8, 48 86.8 / 91.4, 52 91.9 / 91.0;  49k, 48: n 1 31.4 / 32.7, n 4 45.2 / 42.6
+    //   4 / 2:  n 4, 128k   90 136.9 / 166.4, 110 167.2 / 179.6;  49k, 100: n 1 47.0 / 54.3, n 4 65.2 / 70.8, 120: 53.4 / 59.2,
+    //           76.8 / 75.1, 148: 59.1 / 57.7, 91.6 / 82.1
+    //   2 / 1:  49k   149: n 1 60.1 / 79.3, n 4 82.2 / 118.1, 300: 103.5 / 113.1, 158.9 / 163.4, 1000: 263.9 / 259.8, 454.3 / 449.6
+    const int C = B <= 18 ? 16 : B <= 52 ? 8 : B <= 105 ? 4 : 2;
     cfg.gridDim = dim3(C, B);
     cfg.blockDim = dim3(kPickThreads);
     at[1].id = cudaLaunchAttributeClusterDimension;
