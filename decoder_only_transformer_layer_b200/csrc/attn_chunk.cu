@@ -19,7 +19,7 @@
 // Per 128-key block and sub-tile: S = Q K^T (M = N = 128, fp32 in TMEM), P = 2^(S' - m) as
 // bf16 over S in TMEM, O += P V (A = P from TMEM). The maximum m is moved, and O rescaled,
 // only when a row's maximum grows by more than 2^8: P <= 2^8 never overflows and O / l does
-// not depend on m. P is rounded to bf16 once: each weight is off by at most 2^-9 of itself,
+// not depend on m. P is rounded to bf16 once: each weight is off by at most 2^-8 of itself,
 // as much as the rounding of the result; l sums the unrounded fp32 values.
 //
 // Work split. Lengths are known on the device only, so every CTA cuts the work for itself:
@@ -30,11 +30,12 @@
 // tile cut between CTAs leaves unnormalised fp32 pieces (O, m, l) in the workspace, which a
 // second kernel joins in the order of the runs, so results do not depend on timing.
 //
-// Measured (B200, 6.56 TB/s copy, 1610 TFLOP/s cuBLAS). A prompt of 8192 rows, 32/8 heads of 128: 502 us,
-// 1,095 TFLOP/s; bound by each sub-tile's chain of scores, softmax and products, two of which overlap (tensor
-// cores and exponentials are busy 56% of the time). 32 sequences of 5-8 rows at 1000-8000 keys: 115 us, 5.4
-// TB/s; bound by the stream of K and V, and by starting and joining (6 and 8 us). 5 rows at 4096: 17 us of
-// latencies. Score blocks of 64 keys, two buffers a sub-tile, would overlap a sub-tile's scores with its own
+// Measured (B200, 6.56 TB/s copy, 1610 TFLOP/s cuBLAS). A prompt of 8192 rows, 32/8 heads of 128: 510 us in the
+// first calls after a pause (1,078 TFLOP/s), 575-583 in seconds of calls, when the power cap holds the SMs at 1.7
+// GHz (cuBLAS does 1370 TFLOP/s then); in both 0.98 M cycles, bound by each sub-tile's chain of scores, softmax
+// and products, two of which overlap (tensor cores and exponentials are busy 56% of the time). 32 sequences of
+// 5-8 rows at 1000-8000 keys: 117 us (5.3 TB/s), 133-136 in seconds of calls (1.6 GHz, same cause); bound by the
+// stream of K and V, and by starting and joining (6 and 8 us). 5 rows at 4096: 17.8 us of latencies. Score blocks of 64 keys, two buffers a sub-tile, would overlap a sub-tile's scores with its own
 // products, but a product with N = 64 costs as much as one with N = 128 and every step's issue comes twice: 610 us.
 //
 // Masked places. Scores outside a row's keys are replaced, so K may hold anything there.
@@ -184,8 +185,9 @@ DEC_HD int lo_key(const ChunkArgs& a, const Seq& s, int t0) {
 }
 
 // What a tile costs beside its blocks (filling the pipeline, the epilogue), in blocks: the runs are
-// equal in tiles' costs. A tile's units are kTileCost for nothing, then one for each block. (A prompt of 8192:
-// 608 us with 1, 553 with 2, 518 with 3, 510 with 4.)
+// equal in tiles' costs. A tile's units are kTileCost for nothing, then one for each block. With 3, 4, 5, 6 and 8:
+// 24 sequences of which 21 decode 33.2, 33.1, 33.9, 35.6, 36.7 us; 1500 rows in a window of 1024 65.2, 63.9, 67.2, 67.5,
+// 65.7; a prompt of 8192 580, 583, 585, 589, 596; 32 sequences of 5-8 rows 135, 136, 136, 136, 138.
 constexpr int kTileCost = 4;
 // The block at which unit u of a tile lies; a run that ends within the first units has none of it.
 DEC_HD int block_at(int u) { return u > kTileCost ? u - kTileCost : 0; }
@@ -209,8 +211,8 @@ DEC_HD int tile_blocks(const ChunkArgs& a, const Seq& s, int t) {
     return hi_key(s, t1) / kKeys - lo_key(a, s, t0) / kKeys + 1;
 }
 
-// So many tiles are summed one by one, which is shorter than the closed form (24 sequences with few rows each: 32.6
-// against 34.5 us; one of 5 rows: 18.2 against 17.5).
+// So many tiles are summed one by one, the closed form is for more. (Without that: 24 sequences with few rows each
+// 34.8 instead of 33.1 us, 1500 rows in a window 65.1 instead of 64.0, but one sequence of 5 rows 17.1 instead of 17.8.)
 constexpr int kFewTiles = 32;
 
 // Units of one kv head of a sequence.
@@ -542,9 +544,9 @@ DEC_DEVINL float max_nan(float a, float b) {
     return d;
 }
 
-// tanh(y) = 1 - 2 / (e^2y + 1), off by some 2^-21, above |y| = 1/4, its Taylor series (next term
-// 2^-18 of the value there) below, so that the error of c tanh(s / c) stays a 2^-18 part of the
-// score whatever the cap.
+// tanh(y) = 1 - 2 / (e^2y + 1), off by some 2^-22 (2^-20 of the value at 1/4), above |y| = 1/4, its Taylor series
+// (next term 62 y^9 / 2835, 2^-21.5 of the value there) below, so that the error of c tanh(s / c) stays
+// below a 2^-18 part of the score whatever the cap.
 DEC_DEVINL float tanh_exact(float y) {
     const float y2 = y * y;
     float r;
@@ -556,7 +558,7 @@ DEC_DEVINL float tanh_exact(float y) {
 
 // After a failure: shared memory and TMEM go to the next CTA only when nothing is in flight into them. Called by the MMA
 // warp, which waits for the products it issued, the last loads into the ring (at most one a stage) and the last Q.
-// Out of line: inside the kernel it costs every call 0.2 us.
+// Out of line: inside the kernel it costs the shortest calls 0.1 us.
 __device__ __noinline__ void drain(Control& ctl, int stages) {
     volatile int* failed = &ctl.failed;
     if ((threadIdx.x & 31) == 0) atomicExch(&g_chunk_err, 1);

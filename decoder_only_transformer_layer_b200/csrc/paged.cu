@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kApThreads, 4) paged_rope_append_kernel(Append
             if (!isv) {
                 if (isq ? a.q_norm != nullptr : a.k_norm != nullptr) {
                     float ss = u.x * u.x + u.y * u.y + u.z * u.z + u.w * u.w + v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
-                    const unsigned group = (LH == 32 ? 0xffffffffu : ((1u << LH) - 1)) << (tid & 31 & ~(LH - 1));
+                    const unsigned group = ((1u << LH) - 1) << (tid & 31 & ~(LH - 1));  // LH is 8 or 16
 #pragma unroll
                     for (int o = LH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
                     const float r = 1.0f / sqrtf(ss / D + a.eps);
