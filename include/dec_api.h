@@ -399,7 +399,8 @@ dec_status paged_rope_append(const float* qkv, int64_t ld, const float* q_norm, 
  * A row that sees no key (a position below 0) gives zeros, and so does one whose scores are all
  * -inf. A cache row whose table entry lies outside [0, n_pages) is not attended. Keys a row
  * does not attend never reach it, whatever the pool holds there (NaN and infinities included).
- * kv_len above 16 * max_pages counts as 16 * max_pages.
+ * kv_len above 16 * max_pages counts as 16 * max_pages. Scores, maxima and sums are fp32; each weight
+ * is rounded to bf16 once before its product with V, and the result once (each by at most 2^-8).
  * Errors: NULL pointer, a bad size, scale not positive, a negative window or softcap, ldq below nq*d
  * or a workspace too small -> INVALID_ARG; more than 16 query heads a kv head, d other than 64 / 128,
  * page_size other than 16, B > 4096, T > 2^30, max_pages > 2^26, n_pages * nkv >= 2^27, scale outside

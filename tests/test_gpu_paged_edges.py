@@ -130,6 +130,11 @@ def test_verify_batches_around_the_ways_of_sharing_the_work(B, n, V):
     check_verify(verify_inputs(B, n, V, 1, B + n))
 
 
+@pytest.mark.parametrize("B,n", [(508, 64), (65535, 0)])
+def test_verify_most_rows(B, n):
+    check_verify(verify_inputs(B, n, 24, 1, 56))
+
+
 # ------------------------------------------------------------------ gqa_chunk_attn
 
 @pytest.mark.parametrize("d,kind", [(128, k) for k in range(1, 11)] + [(64, k) for k in (1, 4, 5, 7)])
@@ -169,6 +174,40 @@ def test_chunk_scores_that_are_not_finite(val, cap):
         inp[1][table[b, j // 16], :, j % 16, 5] = val
     out = check_chunk(inp, cap=cap)
     assert torch.isnan(out).any() == (cap == 0.0)
+
+
+
+@pytest.mark.parametrize("rows", [[(1, 1)], [(3, 40), (1, 600)], [(2, 3000)], [(130, 5000)]], ids=str)
+def test_chunk_rows_whose_scores_are_all_minus_infinity(rows):
+    """Such a row gives zeros, in one piece or in many; under a cap its scores are all the same."""
+    q, kp, vp, table, cu, lens = chunk_inputs(rows, 8, 2, 128, 64)
+    q.abs_().clamp_min_(0.125)
+    kp.fill_(-math.inf)
+    out = torch.full_like(q, 3.0)
+    dec.gqa_chunk_attn(q, kp, vp, ints(table), ints(cu), ints(lens), 0.1, out)
+    dec.check_standalone()
+    assert (out == 0).all()
+    check_chunk((q, kp, vp, table, cu, lens), cap=20.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [0, 1, 500])
+def test_chunk_values_that_are_not_numbers_stay_with_the_rows_that_see_them(window, d):
+    """V holds NaN at the end, next to it, at window's edges and in the middle, in tiles cut into many
+    pieces too: a row's result is NaN in that column exactly where it sees such a key."""
+    rows = [(3, 3000), (200, 1500), (1, 700), (2, 129), (40, 20)]
+    inp = chunk_inputs(rows, 8, 2, d, 66)
+    table = inp[3]
+    for col, (b, j) in enumerate([(0, 2998), (0, 2498), (0, 2999), (1, 900), (1, 1420), (1, 1299), (2, 699), (2, 199),
+                                  (3, 127), (3, 128), (4, 19), (4, 0)]):
+        inp[2][table[b, j // 16], :, j % 16, 5 * col] = float("nan")
+    check_chunk(inp, window=window)
+
+
+
+def test_chunk_most_sequences():
+    rng = np.random.default_rng(65)
+    check_chunk(chunk_inputs([(int(rng.integers(0, 3)), int(rng.integers(2, 40))) for _ in range(4096)], 2, 1, 64, 65))
 
 
 
